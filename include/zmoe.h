@@ -64,7 +64,8 @@ typedef enum {
 
 typedef enum {
   ZMOE_F32 = 0,
-  ZMOE_BF16 = 1
+  ZMOE_BF16 = 1,
+  ZMOE_E4M3 = 2                    /* 8-bit codes with scales beside them: key-value caches only */
 } zmoe_dtype;
 
 /* Library version, as 10000 * major + 100 * minor + patch. */
@@ -427,6 +428,101 @@ ZMOE_API zmoe_status zmoe_decode_stack(const zmoe_stack_layer* layers, int n_lay
                                        const int32_t* ids, const void* tables, const float* gamma0, int N, int V,
                                        float* h, int32_t* layer_idx, float* layer_gates, float* layer_h,
                                        void* layer_x, void* workspace, size_t ws_bytes, zmoe_stream_t stream);
+
+/*
+ * The residual addition, the RMSNorm of the sum and its 8-bit codes in one pass ([DIGEST] item 5: pre-norm
+ * residual blocks; the ZONOS2 page of the sglang-omni cookbook, "Benchmark Results": the served model runs fp8):
+ *   h'[t] = h[t] + delta[t]                                   (fp32 sum, rounded to h_dtype; delta NULL: h' = h)
+ *   x[t]  = h'[t] / sqrt(mean_c h'[t, c]^2 + eps) * gamma     (of the rounded h', in fp32)
+ *   scale = max|x| / 448 over the row (group 0) or over each 128 columns (group 128); at least 2^-126, and 1
+ *           where every x is 0
+ *   codes[t, c] = the E4M3 value nearest x[t, c] * fp32(1 / scale) (ties to even, saturating at 448)
+ * The codes take the fp32 x, before its rounding to x_dtype.  A row that holds a NaN has NaN codes (0x7F) and
+ * scale 1; an infinite h' gives NaN in its own column and 0 elsewhere, as the formula does.
+ *   h, h_out: [T, d] of h_dtype; delta: [T, d] of delta_dtype or NULL; gamma: f32 [d]; x: [T, d] of x_dtype;
+ *   codes: uint8 [T, d]; scales: f32 [T] (group 0) or [T, d / 128].  h_out, x and (codes with scales) are optional
+ *   (NULL), at least one is given.  h_out may be h or delta (of the same type).
+ *   d % 8 == 0 (group 128: d % 128 == 0), d <= 32768; 16-byte aligned pointers.
+ */
+ZMOE_API zmoe_status zmoe_add_rmsnorm(const void* h, zmoe_dtype h_dtype, const void* delta, zmoe_dtype delta_dtype,
+                                      const float* gamma, float eps, int T, int d, void* h_out, void* x,
+                                      zmoe_dtype x_dtype, uint8_t* codes, float* scales, int group,
+                                      zmoe_stream_t stream);
+
+/*
+ * Appends keys and values to a paged cache, queries and keys normed and rotated by position on the way
+ * ([DIGEST] item 5: grouped-query attention with rotary positions; "Builds on" lists the rotary embedding and
+ * query/key norms).  Token t is at position p = pos[t] of sequence s = seq[t] (seq NULL: s = t).  Per head:
+ *   y = x / sqrt(mean_c x_c^2 + eps) * gamma                  (queries with q_gamma, keys with k_gamma; NULL: y = x)
+ *   the first rotary_dim columns of queries and keys are turned pair by pair by w = p * inv_freq[i]:
+ *     (y_a, y_b) <- (y_a cos w - y_b sin w, y_a sin w + y_b cos w)
+ *     with (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved != 0
+ *   row p % page_size of page page_table[s, p / page_size] receives the key and the value (rounded once, to bf16,
+ *   or to E4M3 codes of value * fp32(1 / scale of the key-value head), saturating at 448); q_out the query.
+ *   q: [T, Hq, D] or NULL, k, v: [T, Hkv, D], of in_dtype (f32 or bf16): heads contiguous, tokens q_stride,
+ *   k_stride and v_stride elements apart (multiples of 16 bytes), so that they may lie in one packed projection.
+ *   inv_freq: f64 [rotary_dim / 2] (NULL when rotary_dim == 0): the angle is reduced in 64 bits.
+ *   q_gamma, k_gamma: f32 [D] or NULL.  q_out: bf16 [T, Hq, D].
+ *   k_cache, v_cache: [n_pages, Hkv, page_size, D] of kv_dtype (ZMOE_BF16, or ZMOE_E4M3: uint8 codes with
+ *   k_scale, v_scale f32 [Hkv]); page_table: int32 [n_seqs, max_pages].
+ *   A token with seq[t] < 0 is padding: nothing of it is stored.  A token whose sequence, position or page is out
+ *   of range counts a device error, and nothing of it is stored.  The (sequence, position) pairs of one call name
+ *   different cache rows; a row named twice holds a mixture of the two tokens.
+ *   D = 64 or 128 (else ZMOE_ERR_UNSUPPORTED), rotary_dim % 16 == 0, page_size % 16 == 0, 16-byte aligned pointers.
+ */
+ZMOE_API zmoe_status zmoe_kv_append(const void* q, const void* k, const void* v, zmoe_dtype in_dtype, int64_t q_stride,
+                                    int64_t k_stride, int64_t v_stride, const int32_t* seq, const int32_t* pos,
+                                    const double* inv_freq, int rotary_dim, int interleaved, const float* q_gamma,
+                                    const float* k_gamma, float eps, int T, int Hq, int Hkv, int D, void* q_out,
+                                    void* k_cache, void* v_cache, zmoe_dtype kv_dtype, const float* k_scale,
+                                    const float* v_scale, const int32_t* page_table, int n_seqs, int max_pages,
+                                    int n_pages, int page_size, zmoe_stream_t stream);
+
+/* Bytes of workspace zmoe_paged_attention needs for these sizes (0 for bad arguments). */
+ZMOE_API size_t zmoe_paged_attention_workspace_size(int B, int Hq, int Hkv, int D);
+
+/*
+ * Attention of one new token per sequence over the paged cache of zmoe_kv_append ([DIGEST] item 5:
+ * grouped-query attention with headwise gating).  Sequence b has n = lens[b] cached tokens (the new one among
+ * them); query head i reads key-value head i / (Hq / Hkv):
+ *   s_t = scale * q[b, i] . k_t;   o = sum_{t<n} exp(s_t) v_t / sum_{t<n} exp(s_t);   lse[b, i] = log sum_t exp(s_t)
+ *   out[b, i] = sigmoid(gate[b, i]) * o             (gate NULL: out = o), rounded once to out_dtype
+ *   q: bf16 [B, Hq, D]; k_cache, v_cache, k_scale, v_scale, page_table [B, max_pages]: as zmoe_kv_append;
+ *   lens: int32 [B] on the device; gate: f32 [B, Hq] or NULL; out: [B, Hq, D] of out_dtype; lse: f32 [B, Hq] or NULL.
+ *   lens[b] <= 0 gives a row of zeros and lse -inf.  A length beyond max_pages * page_size counts a device error and
+ *   is cut to that; the tokens of a page id outside [0, n_pages) count a device error and are left out.  When every
+ *   token is left out (or scores -inf) the row is zeros and lse -inf.  What a page holds behind the sequence's end is
+ *   read but never used, NaN included.
+ *   fp32 accumulation; the results do not depend on the order in which CTAs finish.  Two launches on `stream`.  The
+ *   workspace (16-byte aligned) belongs to one call at a time: calls that may overlap need one each.
+ *   Hq % Hkv == 0, D = 64 or 128 (else ZMOE_ERR_UNSUPPORTED), page_size % 16 == 0, n_pages * Hkv * page_size < 2^32 - 1.
+ */
+ZMOE_API zmoe_status zmoe_paged_attention(const void* q, const void* k_cache, const void* v_cache, zmoe_dtype kv_dtype,
+                                          const float* k_scale, const float* v_scale, const int32_t* page_table,
+                                          const int32_t* lens, const float* gate, float scale, int B, int Hq, int Hkv,
+                                          int D, int max_pages, int n_pages, int page_size, void* out,
+                                          zmoe_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes,
+                                          zmoe_stream_t stream);
+
+/*
+ * Penalties for repeated ids, biases and a mask of allowed ids on the codebook logits, and the greedy id of the
+ * adjusted row ([COOKBOOK] request parameters: repetition penalty; [DIGEST] items 1 and 5).  Per stream t, codebook
+ * n and id v, with c = #{l < hist_lens[t] : history[t, l, n] == v}, each step rounded to fp32:
+ *   z = logits[t, n, v];   c > 0:  z = z > 0 ? z / repetition[t] : z * repetition[t]
+ *   z = z - frequency[t] * c;   c > 0:  z = z - presence[t];   z = z + bias[n, v];   -inf where the mask's bit is 0
+ *   out[t, n, v] = z rounded to dtype
+ *   ids[t, n] = the lowest v with the largest out among the ids that the mask allows and that are not NaN; -1 when
+ *   there is none.
+ *   logits, out: [T, N, V] of dtype (out may be logits); history: int32 [T, L, N] or NULL (frames of ids, oldest
+ *   or newest first; a negative id is no id, an id >= V counts a device error and is left out); hist_lens: int32 [T]
+ *   or NULL (= L), cut to [0, L]; repetition, presence, frequency: f32 [T] or NULL (that step is left out; any of them
+ *   needs history); bias: f32 [N, V] or NULL; mask: bits of uint32 [T, N, ceil(V / 32)], id v at bit v % 32 of word
+ *   v / 32, or NULL; ids: int32 [T, N] or NULL.  L <= 65535.  No workspace, one launch.
+ */
+ZMOE_API zmoe_status zmoe_adjust_logits(const void* logits, zmoe_dtype dtype, const int32_t* history,
+                                        const int32_t* hist_lens, const float* repetition, const float* presence,
+                                        const float* frequency, const float* bias, const uint32_t* mask, int T, int N,
+                                        int V, int L, void* out, int32_t* ids, zmoe_stream_t stream);
 
 /*
  * Reads and clears the device error counters of the current device.  Synchronises

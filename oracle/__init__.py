@@ -27,8 +27,11 @@ from .heads import head_logits, greedy, output_heads
 from .speaker import speaker_prefix
 from .fp8 import (e4m3_decode, e4m3_encode, dequantize_rows, moe_layer_fp8, moe_layer_w8a8,
                   quantize_rows_dynamic)
+from .attention import append_rows, attend, paged_rows, rotate
+from .logits import adjust_logits, allowed_greedy, mask_bits
 
 __all__ = [
+    "append_rows", "attend", "paged_rows", "rotate", "adjust_logits", "allowed_greedy", "mask_bits",
     "delay_shear", "delay_unshear", "embed_sum", "rmsnorm", "embed_sum_rmsnorm",
     "router_logits", "softmax", "select_topk", "route", "permute", "silu", "swiglu_ffn",
     "grouped_swiglu", "combine", "moe_layer", "moe_layer_bruteforce", "decode_stack_step",

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libzmoe.so")
 
 ZMOE_F32 = 0
 ZMOE_BF16 = 1
+ZMOE_E4M3 = 2
 
 STATUS_NAMES = {0: "ZMOE_OK", 1: "ZMOE_ERR_INVALID_ARG", 2: "ZMOE_ERR_UNSUPPORTED", 3: "ZMOE_ERR_CUDA",
                 4: "ZMOE_ERR_WORKSPACE_TOO_SMALL", 5: "ZMOE_ERR_DEVICE_CHECK", 6: "ZMOE_ERR_TIMEOUT"}
@@ -28,6 +29,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _S = ctypes.c_size_t
+_L = ctypes.c_int64
 SIGNATURES = {
     "zmoe_version": (_I, []),
     "zmoe_status_string": (ctypes.c_char_p, [_I]),
@@ -64,6 +66,13 @@ SIGNATURES = {
                                  _P, _P, _P, _S, _P]),
     "zmoe_moe_layer_f16h": (_I, [_P, _P, _P, _F, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                                  _P, _S, _P]),
+    "zmoe_add_rmsnorm": (_I, [_P, _I, _P, _I, _P, _F, _I, _I, _P, _P, _I, _P, _P, _I, _P]),
+    "zmoe_kv_append": (_I, [_P, _P, _P, _I, _L, _L, _L, _P, _P, _P, _I, _I, _P, _P, _F, _I, _I, _I, _I, _P, _P, _P, _I,
+                            _P, _P, _P, _I, _I, _I, _I, _P]),
+    "zmoe_paged_attention_workspace_size": (_S, [_I, _I, _I, _I]),
+    "zmoe_paged_attention": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I, _I, _I, _P, _I, _P, _P,
+                                  _S, _P]),
+    "zmoe_adjust_logits": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
     "zmoe_decode_stack": (_I, [_P, _I, _I, _I, _F, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _S, _P]),
 }
 
@@ -568,6 +577,232 @@ def zmoe_decode_stack(layers, h: torch.Tensor, eps: float = 1e-6, ids: Optional[
                                    workspace.numel() * workspace.element_size(), _stream(stream)),
            "zmoe_decode_stack")
     return h
+
+
+def _shape(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> None:
+    """An optional contiguous CUDA tensor of exactly this type, shape and device."""
+    if t is None:
+        return
+    _need(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {device}")
+
+
+class _On:
+    """Runs a call on the tensors' device: its current stream (unless a stream is given), its kernels."""
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        self.other = self.device.index != torch.cuda.current_device()
+        if self.other:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        if self.stream is not None and self.stream.device != self.device:
+            self.__exit__(None, None, None)
+            raise ValueError(f"the stream is on {self.stream.device}, the call's tensors are on {self.device}")
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.other:
+            self.guard.__exit__(*exc)
+
+
+def zmoe_add_rmsnorm(h: torch.Tensor, gamma: torch.Tensor, delta: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     out_dtype: torch.dtype = torch.bfloat16, want_codes: bool = False, group: int = 0,
+                     outs: Optional[dict] = None, stream=None) -> dict:
+    """h' = h + delta, x = RMSNorm(h') * gamma and x's E4M3 codes with a scale per row (group 0) or per 128 columns.
+
+    Returns dict(h=, x=, codes=uint8, scales=f32 [T, 1] or [T, d / 128]).  With ``outs`` the outputs are the
+    preallocated tensors it holds under those names (h may be ``h`` itself) and nothing else is computed;
+    without it h (when there is a delta), x and, with want_codes, the codes are allocated."""
+    _need(h, "h", None, 2)
+    T, d = h.shape
+    dev = h.device
+    _shape(gamma, "gamma", torch.float32, (d,), dev)
+    if delta is not None:
+        _shape(delta, "delta", delta.dtype, (T, d), dev)
+    ns = d // group if group else 1
+    if outs is None:
+        outs = dict(x=torch.empty((T, d), dtype=out_dtype, device=dev))
+        if delta is not None:
+            outs["h"] = torch.empty_like(h)
+        if want_codes:
+            outs["codes"] = torch.empty((T, d), dtype=torch.uint8, device=dev)
+            outs["scales"] = torch.empty((T, ns), dtype=torch.float32, device=dev)
+    ho, x, codes, scales = outs.get("h"), outs.get("x"), outs.get("codes"), outs.get("scales")
+    _shape(ho, "outs['h']", h.dtype, (T, d), dev)
+    if x is not None:
+        _shape(x, "outs['x']", x.dtype, (T, d), dev)
+        out_dtype = x.dtype
+    _shape(codes, "outs['codes']", torch.uint8, (T, d), dev)
+    _shape(scales, "outs['scales']", torch.float32, (T, ns), dev)
+    with _On(dev, stream) as s:
+        _check(lib().zmoe_add_rmsnorm(_ptr(h), _dtype_code(h.dtype), _ptr(delta),
+                                      _dtype_code(delta.dtype) if delta is not None else ZMOE_F32, _ptr(gamma),
+                                      float(eps), T, d, _ptr(ho), _ptr(x), _dtype_code(out_dtype), _ptr(codes),
+                                      _ptr(scales), group, s), "zmoe_add_rmsnorm")
+    return dict(h=ho, x=x, codes=codes, scales=scales)
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, page_table):
+    """Checks a paged cache; returns (kv dtype code, n_pages, Hkv, page_size, D)."""
+    _need(k_cache, "k_cache", None, 4)
+    dev = k_cache.device
+    if k_cache.dtype not in (torch.bfloat16, torch.uint8):
+        raise TypeError(f"k_cache must be bfloat16 or uint8 (E4M3 codes), got {k_cache.dtype}")
+    _shape(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev)
+    n_pages, Hkv, page_size, D = k_cache.shape
+    _shape(k_scale, "k_scale", torch.float32, (Hkv,), dev)
+    _shape(v_scale, "v_scale", torch.float32, (Hkv,), dev)
+    _need(page_table, "page_table", torch.int32, 2)
+    if page_table.device != dev:
+        raise ValueError(f"page_table is on {page_table.device}, the cache on {dev}")
+    return (ZMOE_E4M3 if k_cache.dtype == torch.uint8 else ZMOE_BF16), n_pages, Hkv, page_size, D
+
+
+def _heads(t: torch.Tensor, name: str, T: int, H: int, D: int, dtype, device) -> int:
+    """A [T, H, D] view whose heads are contiguous; returns the elements between its tokens."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} must have shape {(T, H, D)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    s0, s1, s2 = t.stride()
+    if T and ((D > 1 and s2 != 1) or (H > 1 and s1 != D)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+    return s0 if T > 1 else H * D
+
+
+def zmoe_kv_append(k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   page_table: torch.Tensor, q: Optional[torch.Tensor] = None, seq: Optional[torch.Tensor] = None,
+                   inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
+                   q_gamma: Optional[torch.Tensor] = None, k_gamma: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                   q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Stores rotated keys and values in a paged cache; returns the rotated queries bf16 [T, Hq, D] (None without q).
+
+    q [T, Hq, D], k, v [T, Hkv, D]: f32 or bf16 views of a packed projection; pos int32 [T]; seq int32 [T] (None:
+    token t is sequence t's; negative: padding); k_cache, v_cache [n_pages, Hkv, page_size, D] bf16, or uint8
+    E4M3 codes with k_scale, v_scale f32 [Hkv]; page_table int32 [n_seqs, max_pages]; inv_freq f64 [rotary_dim / 2]."""
+    kv, n_pages, Hkv, page_size, D = _cache_args(k_cache, v_cache, k_scale, v_scale, page_table)
+    dev = k_cache.device
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must have 3 dims")
+    T, dt = k.shape[0], k.dtype
+    ks, vs = _heads(k, "k", T, Hkv, D, dt, dev), _heads(v, "v", T, Hkv, D, dt, dev)
+    Hq = qs = 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must have 3 dims")
+        Hq = q.shape[1]
+        qs = _heads(q, "q", T, Hq, D, dt, dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _shape(q_out, "q_out", torch.bfloat16, (T, Hq, D), dev)
+    _shape(pos, "pos", torch.int32, (T,), dev)
+    _shape(seq, "seq", torch.int32, (T,), dev)
+    _shape(q_gamma, "q_gamma", torch.float32, (D,), dev)
+    _shape(k_gamma, "k_gamma", torch.float32, (D,), dev)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _shape(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
+    with _On(dev, stream) as s:
+        _check(lib().zmoe_kv_append(_ptr(q), _ptr(k), _ptr(v), _dtype_code(dt), qs, ks, vs, _ptr(seq), _ptr(pos),
+                                    _ptr(inv_freq) if rot else None, rot, int(interleaved), _ptr(q_gamma),
+                                    _ptr(k_gamma), float(eps), T, Hq, Hkv, D, _ptr(q_out), _ptr(k_cache),
+                                    _ptr(v_cache), kv, _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+                                    page_table.shape[0], page_table.shape[1], n_pages, page_size, s),
+               "zmoe_kv_append")
+    return q_out
+
+
+def zmoe_paged_attention_workspace_size(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().zmoe_paged_attention_workspace_size(B, Hq, Hkv, D))
+
+
+def zmoe_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                         lens: torch.Tensor, scale: Optional[float] = None, k_scale: Optional[torch.Tensor] = None,
+                         v_scale: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                         out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                         lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence: q bf16 [B, Hq, D] over lens[b] cached tokens -> [B, Hq, D].
+
+    page_table int32 [B, max_pages], lens int32 [B]; scale defaults to 1 / sqrt(D); gate f32 [B, Hq]: the output
+    times sigmoid(gate); lse f32 [B, Hq] receives the log of the sum of exp(scores)."""
+    kv, n_pages, Hkv, page_size, D = _cache_args(k_cache, v_cache, k_scale, v_scale, page_table)
+    dev = k_cache.device
+    _need(q, "q", torch.bfloat16, 3)
+    B, Hq, _ = q.shape
+    _shape(q, "q", torch.bfloat16, (B, Hq, D), dev)
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table has {page_table.shape[0]} rows for {B} sequences")
+    if lens is None:
+        raise ValueError("lens is needed")
+    _shape(lens, "lens", torch.int32, (B,), dev)
+    _shape(gate, "gate", torch.float32, (B, Hq), dev)
+    _shape(lse, "lse", torch.float32, (B, Hq), dev)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=out_dtype, device=dev)
+    _shape(out, "out", out.dtype, (B, Hq, D), dev)
+    with _On(dev, stream) as s:
+        ws_bytes = zmoe_paged_attention_workspace_size(B, Hq, Hkv, D)
+        if workspace is None:
+            workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+        _need(workspace, "workspace")
+        _check(lib().zmoe_paged_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), kv, _ptr(k_scale), _ptr(v_scale),
+                                          _ptr(page_table), _ptr(lens), _ptr(gate),
+                                          float(D ** -0.5 if scale is None else scale), B, Hq, Hkv, D,
+                                          page_table.shape[1], n_pages, page_size, _ptr(out), _dtype_code(out.dtype),
+                                          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), s),
+               "zmoe_paged_attention")
+    return out
+
+
+def zmoe_adjust_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = None,
+                       hist_lens: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                       presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None, stream=None):
+    """Penalties by the ids' counts in history int32 [T, L, N], bias f32 [N, V] and a bit mask int32
+    [T, N, ceil(V / 32)] of allowed ids on logits [T, N, V]; returns (out, ids int32 [T, N]).
+
+    repetition, presence, frequency: f32 [T]; ``out`` may be ``logits``.  ids: the lowest id of the largest
+    adjusted logit, -1 when the mask leaves none."""
+    _need(logits, "logits", None, 3)
+    T, N, V = logits.shape
+    dev = logits.device
+    L = 0
+    if history is not None:
+        _need(history, "history", torch.int32, 3)
+        L = history.shape[1]
+        _shape(history, "history", torch.int32, (T, L, N), dev)
+    _shape(hist_lens, "hist_lens", torch.int32, (T,), dev)
+    for t, name in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
+        _shape(t, name, torch.float32, (T,), dev)
+    _shape(bias, "bias", torch.float32, (N, V), dev)
+    _shape(mask, "mask", torch.int32, (T, N, (V + 31) // 32), dev)
+    if out is None:
+        out = torch.empty_like(logits)
+    if ids is None:
+        ids = torch.empty((T, N), dtype=torch.int32, device=dev)
+    _shape(out, "out", logits.dtype, (T, N, V), dev)
+    _shape(ids, "ids", torch.int32, (T, N), dev)
+    with _On(dev, stream) as s:
+        _check(lib().zmoe_adjust_logits(_ptr(logits), _dtype_code(logits.dtype), _ptr(history), _ptr(hist_lens),
+                                        _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias), _ptr(mask), T,
+                                        N, V, L, _ptr(out), _ptr(ids), s), "zmoe_adjust_logits")
+    return out, ids
 
 
 def zmoe_get_device_errors(stream=None) -> int:
