@@ -9,26 +9,23 @@
 // once, on its way out.
 //
 // Bound by HBM: h and delta are read once, h', x and the codes written once.  A row stays in its threads'
-// registers between the two reductions (sum of squares, largest magnitude), 8 columns (one 16-byte load of
-// bf16, two of f32) a vector, VPT vectors a thread.
-#include <cuda_fp8.h>
-
-#include "common.cuh"
+// registers between the two reductions (sum of squares, largest magnitude).  A thread takes chunks of CH
+// neighbouring columns: 16 where h and delta are both bf16 (two 16-byte loads each; half the shuffles and scales a
+// column that 8 take), 8 otherwise (an f32 chunk of 8 is two 16-byte loads already).
+#include "vectors.cuh"
 
 namespace zmoe {
 namespace {
 
-constexpr int kMaxVpt = 8;
 constexpr int kRowThreads = 512;   // threads a row is spread over at most
-constexpr int kMaxD = kRowThreads * kMaxVpt * 8;
+constexpr int kMaxD = 32768;       // 512 threads with 64 columns each
 
 struct AddNormArgs {
   const void* h;
   const void* delta;    // or null
   const float* gamma;
-  float eps;
+  float eps, inv_d;
   int T, d;
-  int tpr;              // threads per row (a multiple of 32)
   int group;            // columns per scale: 0 = the row, 128
   void* h_out;          // or null
   void* x;              // or null
@@ -36,159 +33,165 @@ struct AddNormArgs {
   float* scales;
 };
 
-__device__ __forceinline__ void load8(const uint16_t* p, float* v) { unpack_bf16x8(*reinterpret_cast<const uint4*>(p), v); }
-
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                            pack_bf16x2(v[6], v[7]));
-}
-
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-__device__ __forceinline__ float round_to(uint16_t*, float v) { return bf16_to_f32(f32_to_bf16_bits(v)); }
-__device__ __forceinline__ float round_to(float*, float v) { return v; }
-
 // The scale of values whose largest magnitude is amax; never so small that its reciprocal overflows.
 __device__ __forceinline__ float code_scale(float amax) {
   return amax > 0.f ? fmaxf(__fdiv_rn(amax, 448.f), 1.17549435e-38f) : 1.f;
 }
 
-__device__ __forceinline__ uint2 encode8(const float* v, float r) {
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v[4 * i], r), __fmul_rn(v[4 * i + 1], r)),
-                                                __NV_SATFINITE, __NV_E4M3);
-    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v[4 * i + 2], r), __fmul_rn(v[4 * i + 3], r)),
-                                                __NV_SATFINITE, __NV_E4M3);
-    w[i] = (a & 0xFFFFu) | (b << 16);
-  }
-  return make_uint2(w[0], w[1]);
-}
-
-// One row per tpr threads; blockDim.x / tpr rows per block.
-template <typename TH, typename TD, typename TX, int VPT>
+// One row per blockDim.x threads (a multiple of 32), blockDim.y rows per block.
+template <typename TH, typename TD, typename TX, int CH, int N>
 __global__ void __launch_bounds__(kRowThreads) add_rmsnorm_kernel(AddNormArgs a) {
+  constexpr int kVecs = CH / 8;      // vectors of 8 columns a chunk
   __shared__ float red[2][kRowThreads / 32];
-  const int warps_row = a.tpr >> 5;
-  const int r_in_block = threadIdx.x / a.tpr, t_in_row = threadIdx.x - r_in_block * a.tpr;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / a.tpr) + r_in_block;
-  const int vecs = a.d >> 3;
-  const bool live = row < a.T;
-  const size_t base = static_cast<size_t>(live ? row : 0) * a.d;
+  const int warps_row = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* red_row[2] = {red[0] + threadIdx.y * warps_row, red[1] + threadIdx.y * warps_row};
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const size_t base = static_cast<size_t>(row < a.T ? row : 0) * a.d;
+  const int end = row < a.T ? a.d : 0;   // columns from here on are not there
   const TH* h = static_cast<const TH*>(a.h) + base;
   const TD* dl = static_cast<const TD*>(a.delta) + base;
-  float v[VPT][8];
+  const int c0 = threadIdx.x * CH, step = blockDim.x * CH;
+  Raw8<TH> raw[N][kVecs];
+  float v[N][kVecs][8];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (t_in_row + i * a.tpr) * 8;
-    const bool on = live && c < a.d;
+  for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-    if (on) load8(h + c, v[i]);
-  }
-  if (a.delta) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (t_in_row + i * a.tpr) * 8;
-      if (live && c < a.d) {
-        float w[8];
-        load8(dl + c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = round_to(static_cast<TH*>(nullptr), v[i][e] + w[e]);
-      }
+    for (int k = 0; k < kVecs; ++k) {
+      const int c = c0 + i * step + 8 * k;
+      if (c < end) raw[i][k].load(h + c);
+      else raw[i][k].clear();
     }
+  if (a.delta) {
+    Raw8<TD> add[N][kVecs];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        const int c = c0 + i * step + 8 * k;
+        if (c < end) add[i][k].load(dl + c);
+        else add[i][k].clear();
+      }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        float w[8];
+        raw[i][k].get(v[i][k]);
+        add[i][k].get(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][k][e] += w[e];
+        raw[i][k].put(v[i][k]);
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) raw[i][k].get(v[i][k]);
   }
   float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (t_in_row + i * a.tpr) * 8;
-    if (a.h_out && live && c < a.d) store8(static_cast<TH*>(a.h_out) + base + c, v[i]);
+  for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-  }
+    for (int k = 0; k < kVecs; ++k) {
+      const int c = c0 + i * step + 8 * k;
+      if (a.h_out && c < end) raw[i][k].store(static_cast<TH*>(a.h_out) + base + c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[i][k][e], v[i][k][e], ss);
+    }
   ss = warp_sum(ss);
   if (warps_row > 1) {
-    if (lane == 0) red[0][warp] = ss;
+    if (lane == 0) red_row[0][warp] = ss;
     __syncthreads();
-    ss = warp_sum(lane < warps_row ? red[0][r_in_block * warps_row + lane] : 0.f);
+    ss = warp_sum(lane < warps_row ? red_row[0][lane] : 0.f);
   }
-  const float inv = rsqrtf(ss / static_cast<float>(a.d) + a.eps);
-  float amax = 0.f;
+  const float inv = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+  float amax[N];   // of a chunk
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (t_in_row + i * a.tpr) * 8;
-    if (live && c < a.d) {
-      float g[8];
-      load8(a.gamma + c, g);
+  for (int i = 0; i < N; ++i) {
+    amax[i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[i][e] = v[i][e] * inv * g[e];
-        amax = fmaxf(amax, fabsf(v[i][e]));
+    for (int k = 0; k < kVecs; ++k) {
+      const int c = c0 + i * step + 8 * k;
+      if (c < end) {
+        const float4 g0 = __ldg(reinterpret_cast<const float4*>(a.gamma + c));
+        const float4 g1 = __ldg(reinterpret_cast<const float4*>(a.gamma + c) + 1);
+        const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[i][k][e] = v[i][k][e] * inv * g[e];
+          amax[i] = fmaxf(amax[i], fabsf(v[i][k][e]));
+        }
+        if (a.x) store8(static_cast<TX*>(a.x) + base + c, v[i][k]);
       }
-      if (a.x) store8(static_cast<TX*>(a.x) + base + c, v[i]);
     }
   }
   if (!a.codes) return;   // uniform over the grid
   if (a.group == 0) {
+    float top = amax[0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int i = 1; i < N; ++i) top = fmaxf(top, amax[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (warps_row > 1) {
-      if (lane == 0) red[1][warp] = amax;
+      if (lane == 0) red_row[1][warp] = top;
       __syncthreads();
-      amax = lane < warps_row ? red[1][r_in_block * warps_row + lane] : 0.f;
+      top = lane < warps_row ? red_row[1][lane] : 0.f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
-    const float s = code_scale(amax), r = __frcp_rn(s);
+    const float s = code_scale(top), r = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (t_in_row + i * a.tpr) * 8;
-      if (live && c < a.d) *reinterpret_cast<uint2*>(a.codes + base + c) = encode8(v[i], r);
-    }
-    if (live && t_in_row == 0) a.scales[row] = s;
-  } else {   // 128 columns = 16 neighbouring lanes
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int vec = t_in_row + i * a.tpr, c = vec * 8;
-      float m = 0.f;
+      for (int k = 0; k < kVecs; ++k) {
+        const int c = c0 + i * step + 8 * k;
+        if (c < end)
+          *reinterpret_cast<uint2*>(a.codes + base + c) = make_uint2(e4m3x4(v[i][k], r), e4m3x4(v[i][k] + 4, r));
+      }
+    if (row < a.T && threadIdx.x == 0) a.scales[row] = s;
+  } else {   // 128 columns = 128 / CH neighbouring lanes
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[i][e]));
+    for (int i = 0; i < N; ++i) {
+      const int c = c0 + i * step;
+      float top = amax[i];
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (live && vec < vecs) {
-        const float s = code_scale(m);
-        *reinterpret_cast<uint2*>(a.codes + base + c) = encode8(v[i], __frcp_rn(s));
-        if ((vec & 15) == 0) a.scales[static_cast<size_t>(row) * (a.d >> 7) + (vec >> 4)] = s;
+      for (int o = 64 / CH; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (c < end) {   // d % 128 == 0: whole chunks
+        const float s = code_scale(top), r = __frcp_rn(s);
+        uint32_t w[2 * kVecs];
+#pragma unroll
+        for (int k = 0; k < 2 * kVecs; ++k) w[k] = e4m3x4(v[i][k >> 1] + 4 * (k & 1), r);
+        if (kVecs == 2) *reinterpret_cast<uint4*>(a.codes + base + c) = make_uint4(w[0], w[1], w[2 * kVecs - 2], w[2 * kVecs - 1]);
+        else *reinterpret_cast<uint2*>(a.codes + base + c) = make_uint2(w[0], w[1]);
+        if ((c & 127) == 0) a.scales[static_cast<size_t>(row) * (a.d >> 7) + (c >> 7)] = s;
       }
     }
   }
 }
 
-template <typename TH, typename TD, typename TX>
-void launch_vpt(const AddNormArgs& a, int vpt, int block, int grid, cudaStream_t s) {
-  switch (vpt) {
-    case 1: add_rmsnorm_kernel<TH, TD, TX, 1><<<grid, block, 0, s>>>(a); break;
-    case 2: add_rmsnorm_kernel<TH, TD, TX, 2><<<grid, block, 0, s>>>(a); break;
-    case 4: add_rmsnorm_kernel<TH, TD, TX, 4><<<grid, block, 0, s>>>(a); break;
-    default: add_rmsnorm_kernel<TH, TD, TX, 8><<<grid, block, 0, s>>>(a); break;
+// Chunks a thread holds: one as long as 512 threads reach a row's end (N = 1, 2, 4, 8).
+template <typename TH, typename TD, typename TX, int CH>
+void launch_row(const AddNormArgs& a, cudaStream_t s) {
+  const int chunks = (a.d + CH - 1) / CH;
+  static const int pref = getenv("PREF") ? atoi(getenv("PREF")) : 256;
+  int n = 1;
+  while (chunks > pref * n && n * CH < 64) n *= 2;
+  const int threads = ((chunks + n - 1) / n + 31) / 32 * 32;
+  const dim3 block(threads, threads >= 256 ? 1 : 256 / threads);
+  const int grid = (a.T + block.y - 1) / block.y;
+  switch (n) {
+    case 1: add_rmsnorm_kernel<TH, TD, TX, CH, 1><<<grid, block, 0, s>>>(a); break;
+    case 2: add_rmsnorm_kernel<TH, TD, TX, CH, 2><<<grid, block, 0, s>>>(a); break;
+    case 4: add_rmsnorm_kernel<TH, TD, TX, CH, 4><<<grid, block, 0, s>>>(a); break;
+    default: add_rmsnorm_kernel<TH, TD, TX, CH, 64 / CH><<<grid, block, 0, s>>>(a); break;
   }
 }
 
 template <typename TH, typename TD>
-void launch_x(const AddNormArgs& a, zmoe_dtype xt, int vpt, int block, int grid, cudaStream_t s) {
-  if (xt == ZMOE_BF16) launch_vpt<TH, TD, uint16_t>(a, vpt, block, grid, s);
-  else launch_vpt<TH, TD, float>(a, vpt, block, grid, s);
+void launch_x(const AddNormArgs& a, zmoe_dtype xt, cudaStream_t s) {
+  constexpr int CH = sizeof(TH) + sizeof(TD) == 4 ? 16 : 8;
+  if (xt == ZMOE_BF16) launch_row<TH, TD, uint16_t, CH>(a, s);
+  else launch_row<TH, TD, float, CH>(a, s);
 }
 
 }  // namespace
@@ -216,21 +219,14 @@ extern "C" zmoe_status zmoe_add_rmsnorm(const void* h, zmoe_dtype h_dtype, const
                "zmoe_add_rmsnorm: pointers must be 16-byte aligned (scales: 4-byte)");
   if (d > kMaxD) return fail(ZMOE_ERR_UNSUPPORTED, "zmoe_add_rmsnorm: d must be at most 32768");
   clear_error();
-  const int vecs = d / 8;
-  int vpt = 1;
-  while (vecs > kRowThreads * vpt) vpt *= 2;
-  int tpr = (vecs + vpt - 1) / vpt;
-  tpr = (tpr + 31) / 32 * 32;
-  const int rows = tpr >= 256 ? 1 : 256 / tpr;
-  AddNormArgs a{h, delta, gamma, eps, T, d, tpr, group, h_out, x, codes, scales};
-  const int grid = (T + rows - 1) / rows, block = rows * tpr;
+  const AddNormArgs a{h, delta, gamma, eps, 1.f / static_cast<float>(d), T, d, group, h_out, x, codes, scales};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (h_dtype == ZMOE_BF16) {
-    if (delta_dtype == ZMOE_BF16) launch_x<uint16_t, uint16_t>(a, x_dtype, vpt, block, grid, s);
-    else launch_x<uint16_t, float>(a, x_dtype, vpt, block, grid, s);
+    if (delta_dtype == ZMOE_BF16) launch_x<uint16_t, uint16_t>(a, x_dtype, s);
+    else launch_x<uint16_t, float>(a, x_dtype, s);
   } else {
-    if (delta_dtype == ZMOE_BF16) launch_x<float, uint16_t>(a, x_dtype, vpt, block, grid, s);
-    else launch_x<float, float>(a, x_dtype, vpt, block, grid, s);
+    if (delta_dtype == ZMOE_BF16) launch_x<float, uint16_t>(a, x_dtype, s);
+    else launch_x<float, float>(a, x_dtype, s);
   }
   return check_launch("zmoe_add_rmsnorm");
 }

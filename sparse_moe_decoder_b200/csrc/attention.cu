@@ -83,11 +83,24 @@ __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
 
 __device__ __forceinline__ int tiles_of(int n) { return static_cast<int>((static_cast<unsigned>(n) + 15u) >> 4); }
 
-// First tile of warp w's piece of `total` tiles over `warps` warps, and the warp that owns tile x.
-__device__ __forceinline__ long long piece_start(long long w, long long total, int warps) { return w * total / warps; }
-__device__ __forceinline__ int piece_owner(long long x, long long total, int warps) {
-  return static_cast<int>(((x + 1) * warps - 1) / total);
+__device__ __forceinline__ long long divide(long long x, long long y) {   // of numbers that are not negative
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
 }
+
+// `total` tiles in `count` pieces, one a warp, none empty: the first `more` pieces have one tile more.
+struct Pieces {
+  int count;
+  long long size, more;
+
+  __device__ __forceinline__ Pieces(long long total, int warps)
+      : count(total < warps ? static_cast<int>(total) : warps), size(divide(total, count)), more(total - size * count) {}
+  __device__ __forceinline__ long long start(long long w) const { return w * size + (w < more ? w : more); }
+  __device__ __forceinline__ int owner(long long x) const {   // the warp whose piece tile x is in
+    const long long big = more * (size + 1);
+    return static_cast<int>(x < big ? divide(x, size + 1) : more + divide(x - big, size));
+  }
+};
 
 // Exclusive prefix over the block's threads of `mine`; every thread receives the total.
 __device__ __forceinline__ long long block_prefix(long long mine, long long* scratch, long long& total) {
@@ -211,9 +224,10 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
   long long total;
   const long long pre = block_prefix(mine, scan, total);
   if (total == 0) return;
+  const Pieces pieces(total, a.warps);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const long long x = piece_start(static_cast<long long>(blockIdx.x) * kWarps + w, total, a.warps);
+    const long long x = pieces.start(static_cast<long long>(blockIdx.x) * kWarps + w);
     if (x >= pre && x < pre + mine) {
       long long p = pre;
       int b = b_lo;
@@ -228,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
   }
   __syncthreads();
   const long long gw = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  const long long x0 = piece_start(gw, total, a.warps), x1 = piece_start(gw + 1, total, a.warps);
-  if (x0 >= x1) return;
+  if (gw >= pieces.count) return;
+  const long long x0 = pieces.start(gw), x1 = pieces.start(gw + 1);
   int b = at_b[warp], n = seq_len(a, b), nt = tiles_of(n);
   int u = static_cast<int>(at_off[warp] / nt), tile = static_cast<int>(at_off[warp] - static_cast<long long>(u) * nt);
   const int tpp = a.page_size >> 4;   // tiles per page
@@ -540,16 +554,15 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a) {
     return;
   }
   const long long p0 = start_of_b + static_cast<long long>(hk * a.gtiles + gt) * nt, p1 = p0 + nt;
-  const int w0 = piece_owner(p0, total, a.warps), w1 = piece_owner(p1 - 1, total, a.warps);
+  const Pieces pieces(total, a.warps);
+  const int w0 = pieces.owner(p0), w1 = pieces.owner(p1 - 1);
   if (w0 == w1) return;   // written whole
-  const int first_slot = piece_start(w0, total, a.warps) == p0 ? 0 : 1;
+  const int first_slot = pieces.start(w0) == p0 ? 0 : 1;
   auto part_of = [&](int w) -> const float* {
     return a.parts + (static_cast<size_t>(w) * 2 + (w == w0 ? first_slot : 0)) * part_floats<D, HT>();
   };
-  auto empty = [&](int w) { return piece_start(w, total, a.warps) == piece_start(w + 1, total, a.warps); };
   float m = __int_as_float(0xff800000);
-  for (int w = w0 + static_cast<int>(threadIdx.x); w <= w1; w += kThreads)
-    if (!empty(w)) m = fmaxf(m, __ldcg(part_of(w) + head));
+  for (int w = w0 + static_cast<int>(threadIdx.x); w <= w1; w += kThreads) m = fmaxf(m, __ldcg(part_of(w) + head));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red[warp][0] = m;
@@ -561,9 +574,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a) {
   float l = 0.f, acc[kCols];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int w = w0 + warp; w <= w1; w += kWarps) {
-    if (empty(w)) continue;
     const float* p = part_of(w);
     const float k = exp2f(__ldcg(p + head) - base);
     l = fmaf(__ldcg(p + H + head), k, l);

@@ -12,11 +12,11 @@
 // that a far position costs no accuracy; the sine and cosine of the fraction are fp32.  They are formed once
 // per token and pair in shared memory and serve every head of the token.
 //
-// Bound by HBM for prompts, by latency for decode steps.  D / 16 lanes carry a head, 16 columns each (the two
-// halves of its pairs), so a head's sum of squares is a shuffle within its lanes and every access is 16 bytes.
-#include <cuda_fp8.h>
-
-#include "common.cuh"
+// Bound by HBM for prompts, by latency for decode steps.  D / 16 lanes carry a head, 16 columns each (eight of each
+// half of its pairs), so a head's sum of squares is a shuffle within its lanes and every access is 16 bytes.  A
+// group of lanes has two heads in flight; the first are asked for before the positions, so a decode step waits for
+// memory twice: for the inputs and indices, then for the page's id.
+#include "vectors.cuh"
 
 namespace zmoe {
 namespace {
@@ -24,6 +24,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;      // tokens of one block
 constexpr int kMaxHalf = 64;       // pairs of one head (D <= 128)
+constexpr int kAhead = 2;          // heads in flight a group of lanes
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -42,142 +43,161 @@ struct AppendArgs {
   unsigned int* errors;
 };
 
-__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(p), v);
-}
-
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-__device__ __forceinline__ void store8_bf16(uint16_t* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                            pack_bf16x2(v[6], v[7]));
-}
-
-// E4M3 codes of v * r (nearest, saturating), r = fp32(1 / scale).
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float* v, float r) {
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v[4 * i], r), __fmul_rn(v[4 * i + 1], r)),
-                                                __NV_SATFINITE, __NV_E4M3);
-    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v[4 * i + 2], r), __fmul_rn(v[4 * i + 3], r)),
-                                                __NV_SATFINITE, __NV_E4M3);
-    w[i] = (a & 0xFFFFu) | (b << 16);
-  }
-  *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-}
-
 template <typename TI, int D, bool FP8>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 16;                 // lanes of a head
-  __shared__ float2 turn[kMaxTokens][kMaxHalf];  // (cos, sin)
+  constexpr int kGroups = kThreads / kLanes;     // heads at a time
+  __shared__ __align__(16) float2 turn[kMaxTokens][kMaxHalf];   // (cos, sin)
   __shared__ long long slot[kMaxTokens];         // cache row of head 0: page * Hkv * page_size + row; -1: skip
   const int t0 = blockIdx.x * a.tokens;
   const int nt = a.T - t0 < a.tokens ? a.T - t0 : a.tokens;
   const int half = a.rot >> 1;
+  const int q_heads = a.q ? a.Hq : 0, heads = q_heads + 2 * a.Hkv;
+  const int l = threadIdx.x % kLanes;
+  // An item is a head of a token; this lane has its columns c0 .. c0 + 7 and c1 .. c1 + 7.  The heads of the
+  // queries, the keys and the values are numbered one after another.
+  struct Item {
+    int tt, hd;
+    __device__ __forceinline__ void wrap(int heads) {
+      while (hd >= heads) {
+        hd -= heads;
+        ++tt;
+      }
+    }
+  };
+  struct Cols {
+    int kind, hh, c0, c1;   // kind: query, key, value; hh: the head of its kind
+    bool turned;
+  };
+  auto cols_of = [&](const Item& it) {
+    Cols x;
+    x.kind = it.hd < q_heads ? 0 : (it.hd < q_heads + a.Hkv ? 1 : 2);
+    x.hh = it.hd - (x.kind == 0 ? 0 : (x.kind == 1 ? q_heads : q_heads + a.Hkv));
+    x.turned = x.kind < 2 && 16 * l < a.rot;
+    const bool apart = x.turned && !a.interleaved;
+    x.c0 = apart ? 8 * l : 16 * l;
+    x.c1 = x.c0 + (apart ? half : 8);
+    return x;
+  };
+  Raw8<TI> raw[kAhead][2];
+  Item at[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    at[u] = Item{0, static_cast<int>(threadIdx.x) / kLanes + u * kGroups};
+    at[u].wrap(heads);
+  }
+  auto fetch = [&]() {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (at[u].tt < nt) {
+        const Cols x = cols_of(at[u]);
+        const TI* src = static_cast<const TI*>(x.kind == 0 ? a.q : (x.kind == 1 ? a.k : a.v)) +
+                        (t0 + at[u].tt) * (x.kind == 0 ? a.q_stride : (x.kind == 1 ? a.k_stride : a.v_stride)) + x.hh * D;
+        raw[u][0].load(src + x.c0);
+        raw[u][1].load(src + x.c1);
+      }
+    }
+  };
+  fetch();
   if (threadIdx.x < nt) {
     const int t = t0 + threadIdx.x;
-    const int s = a.seq ? a.seq[t] : t;
-    long long at = -1;
+    const int s = a.seq ? __ldg(a.seq + t) : t, p = __ldg(a.pos + t);
+    long long to = -1;
     if (s >= 0) {   // a negative sequence marks a padding token
-      const int p = a.pos[t];
       const bool ok = s < a.n_seqs && p >= 0 && p < static_cast<long long>(a.max_pages) * a.page_size;
-      const int page = ok ? a.page_table[static_cast<size_t>(s) * a.max_pages + p / a.page_size] : -1;
+      const int col = ok ? static_cast<int>(static_cast<unsigned>(p) / static_cast<unsigned>(a.page_size)) : 0;
+      const int page = ok ? __ldg(a.page_table + static_cast<size_t>(s) * a.max_pages + col) : -1;
       if (page >= 0 && page < a.n_pages)
-        at = static_cast<long long>(page) * a.Hkv * a.page_size + p % a.page_size;
+        to = static_cast<long long>(page) * a.Hkv * a.page_size + (p - col * a.page_size);
       else
         record_device_error(a.errors);
     }
-    slot[threadIdx.x] = at;
+    slot[threadIdx.x] = to;
   }
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int t = i / half, f = i - t * half;
-    const double turns = static_cast<double>(a.pos[t0 + t]) * a.inv_freq[f] * 0.15915494309189533577;   // 1 / (2 pi)
-    float sn, cs;
-    sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn, &cs);
-    turn[t][f] = make_float2(cs, sn);
+  for (int i = threadIdx.x; i < kMaxTokens * kMaxHalf; i += kThreads) {
+    const int t = i / kMaxHalf, f = i % kMaxHalf;
+    if (t < nt && f < half) {
+      const double turns =
+          static_cast<double>(__ldg(a.pos + t0 + t)) * __ldg(a.inv_freq + f) * 0.15915494309189533577;   // 1 / (2 pi)
+      float sn, cs;
+      sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn, &cs);
+      turn[t][f] = make_float2(cs, sn);
+    }
   }
   __syncthreads();
-  const int heads = (a.q ? a.Hq : 0) + 2 * a.Hkv, q_heads = heads - 2 * a.Hkv;
-  const int l = threadIdx.x % kLanes;
-  const int items = nt * heads, rounds = (items + kThreads / kLanes - 1) / (kThreads / kLanes);
-  for (int r = 0; r < rounds; ++r) {
-    const int item = r * (kThreads / kLanes) + threadIdx.x / kLanes;
-    const int tt = item / heads, hd = item - tt * heads;
-    const bool live = item < items && slot[tt < nt ? tt : 0] >= 0;
-    const int kind = hd < q_heads ? 0 : (hd < q_heads + a.Hkv ? 1 : 2);   // query, key, value
-    const int hh = kind == 0 ? hd : (kind == 1 ? hd - q_heads : hd - q_heads - a.Hkv);
-    // this lane's two vectors of 8 columns
-    int c0 = 16 * l, c1 = 16 * l + 8;
-    const bool turned = kind < 2 && 16 * l < a.rot;
-    if (!a.interleaved && turned) {
-      c0 = 8 * l;
-      c1 = 8 * l + half;
-    }
-    float x[16];
+  for (int left = nt * heads; left > 0; left -= kAhead * kGroups) {   // every lane takes every round: they shuffle
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.f;
-    if (live) {
-      const TI* src = static_cast<const TI*>(kind == 0 ? a.q : (kind == 1 ? a.k : a.v)) +
-                      static_cast<long long>(t0 + tt) * (kind == 0 ? a.q_stride : (kind == 1 ? a.k_stride : a.v_stride)) +
-                      static_cast<size_t>(hh) * D;
-      load8(src + c0, x);
-      load8(src + c1, x + 8);
-    }
-    const float* gamma = kind == 0 ? a.q_gamma : (kind == 1 ? a.k_gamma : nullptr);
-    float ss = 0.f;
+    for (int u = 0; u < kAhead; ++u) {
+      const int tt = at[u].tt;
+      const Cols it = cols_of(at[u]);
+      float x[16];
+      raw[u][0].get(x);
+      raw[u][1].get(x + 8);
+      const long long to = tt < nt ? slot[tt] : -1;
+      const float* gamma = it.kind == 0 ? a.q_gamma : (it.kind == 1 ? a.k_gamma : nullptr);
+      if (a.q_gamma || a.k_gamma) {   // the whole warp
+        float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!live) continue;
-    if (gamma) {
-      const float inv = rsqrtf(ss / static_cast<float>(D) + a.eps);
-      float g[16];
-      load8(gamma + c0, g);
-      load8(gamma + c1, g + 8);
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (gamma) {
+          const float inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * g[e];
-    }
-    if (turned) {
-      if (a.interleaved) {
+          for (int k = 0; k < 2; ++k) {
+            const float4* gp = reinterpret_cast<const float4*>(gamma + (k ? it.c1 : it.c0));
+            const float4 g0 = __ldg(gp), g1 = __ldg(gp + 1);
+            const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 w = turn[tt][8 * l + e];
-          const float u = x[2 * e], z = x[2 * e + 1];
-          x[2 * e] = u * w.x - z * w.y;
-          x[2 * e + 1] = u * w.y + z * w.x;
+            for (int e = 0; e < 8; ++e) x[8 * k + e] = x[8 * k + e] * inv * g[e];
+          }
         }
-      } else {
+      }
+      if (to < 0) continue;
+      if (it.turned) {
+        const float4* w = reinterpret_cast<const float4*>(&turn[tt][8 * l]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 w = turn[tt][8 * l + e];
-          const float u = x[e], z = x[8 + e];
-          x[e] = u * w.x - z * w.y;
-          x[8 + e] = u * w.y + z * w.x;
+        for (int e = 0; e < 8; e += 2) {
+          const float4 cs = w[e >> 1];   // (cos, sin) of two pairs
+          if (a.interleaved) {
+            const float y0 = x[2 * e], z0 = x[2 * e + 1], y1 = x[2 * e + 2], z1 = x[2 * e + 3];
+            x[2 * e] = y0 * cs.x - z0 * cs.y;
+            x[2 * e + 1] = y0 * cs.y + z0 * cs.x;
+            x[2 * e + 2] = y1 * cs.z - z1 * cs.w;
+            x[2 * e + 3] = y1 * cs.w + z1 * cs.z;
+          } else {
+            const float y0 = x[e], z0 = x[8 + e], y1 = x[e + 1], z1 = x[9 + e];
+            x[e] = y0 * cs.x - z0 * cs.y;
+            x[8 + e] = y0 * cs.y + z0 * cs.x;
+            x[e + 1] = y1 * cs.z - z1 * cs.w;
+            x[9 + e] = y1 * cs.w + z1 * cs.z;
+          }
+        }
+      }
+      if (it.kind == 0) {
+        uint16_t* dst = a.q_out + (static_cast<size_t>(t0 + tt) * a.Hq + it.hh) * D;
+        store8(dst + it.c0, x);
+        store8(dst + it.c1, x + 8);
+      } else {
+        const size_t row = static_cast<size_t>(to + static_cast<long long>(it.hh) * a.page_size) * D;
+        void* cache = it.kind == 1 ? a.k_cache : a.v_cache;
+        if (FP8) {
+          const float rs = __frcp_rn(__ldg((it.kind == 1 ? a.k_scale : a.v_scale) + it.hh));
+          uint8_t* dst = static_cast<uint8_t*>(cache) + row;
+          *reinterpret_cast<uint2*>(dst + it.c0) = make_uint2(e4m3x4(x, rs), e4m3x4(x + 4, rs));
+          *reinterpret_cast<uint2*>(dst + it.c1) = make_uint2(e4m3x4(x + 8, rs), e4m3x4(x + 12, rs));
+        } else {
+          store8(static_cast<uint16_t*>(cache) + row + it.c0, x);
+          store8(static_cast<uint16_t*>(cache) + row + it.c1, x + 8);
         }
       }
     }
-    if (kind == 0) {
-      uint16_t* dst = a.q_out + (static_cast<size_t>(t0 + tt) * a.Hq + hh) * D;
-      store8_bf16(dst + c0, x);
-      store8_bf16(dst + c1, x + 8);
-    } else {
-      const size_t at = static_cast<size_t>(slot[tt] + static_cast<long long>(hh) * a.page_size) * D;
-      void* cache = kind == 1 ? a.k_cache : a.v_cache;
-      if (FP8) {
-        const float rs = __frcp_rn((kind == 1 ? a.k_scale : a.v_scale)[hh]);
-        store8_e4m3(static_cast<uint8_t*>(cache) + at + c0, x, rs);
-        store8_e4m3(static_cast<uint8_t*>(cache) + at + c1, x + 8, rs);
-      } else {
-        store8_bf16(static_cast<uint16_t*>(cache) + at + c0, x);
-        store8_bf16(static_cast<uint16_t*>(cache) + at + c1, x + 8);
-      }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      at[u].hd += kAhead * kGroups;
+      at[u].wrap(heads);
     }
+    fetch();
   }
 }
 

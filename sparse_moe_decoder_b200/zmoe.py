@@ -579,36 +579,51 @@ def zmoe_decode_stack(layers, h: torch.Tensor, eps: float = 1e-6, ids: Optional[
     return h
 
 
-def _shape(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> None:
-    """An optional contiguous CUDA tensor of exactly this type, shape and device."""
+def _at(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int) -> Optional[int]:
+    """The address of a contiguous CUDA tensor of exactly this type (None: any), shape (None: any) and device."""
     if t is None:
-        return
-    _need(t, name, dtype)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {device}")
+        return None
+    if not isinstance(t, torch.Tensor) or (t.dtype is not dtype and dtype is not None) or not t.is_contiguous() or \
+            t.get_device() != dev or (shape is not None and t.shape != shape):
+        _need(t, name, dtype)
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on cuda:{dev}")
+    return t.data_ptr()
 
 
-class _On:
-    """Runs a call on the tensors' device: its current stream (unless a stream is given), its kernels."""
+def _out(shape, dtype, dev: int, stream, shared: bool = True) -> torch.Tensor:
+    """A new tensor for a call on `stream`: from that stream's memory, so that nothing pending elsewhere still uses
+    it; ``shared``: the current stream may use it too before it is reused."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if shared:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
 
-    def __init__(self, device: torch.device, stream):
-        self.device, self.stream = device, stream
 
-    def __enter__(self):
-        self.other = self.device.index != torch.cuda.current_device()
-        if self.other:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        if self.stream is not None and self.stream.device != self.device:
-            self.__exit__(None, None, None)
-            raise ValueError(f"the stream is on {self.stream.device}, the call's tensors are on {self.device}")
-        return _stream(self.stream)
+def _call(name: str, dev: int, stream, *args) -> None:
+    """One C call on the device of its tensors and on its current stream, or on `stream`."""
+    fn = getattr(_lib or lib(), name)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        _on_device(stream, dev)
+        raw = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status:
+        _check(status, name)
 
-    def __exit__(self, *exc):
-        if self.other:
-            self.guard.__exit__(*exc)
+
+def _on_device(stream, dev: int) -> None:
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the call's tensors are on cuda:{dev}")
 
 
 def zmoe_add_rmsnorm(h: torch.Tensor, gamma: torch.Tensor, delta: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -620,60 +635,48 @@ def zmoe_add_rmsnorm(h: torch.Tensor, gamma: torch.Tensor, delta: Optional[torch
     preallocated tensors it holds under those names (h may be ``h`` itself) and nothing else is computed;
     without it h (when there is a delta), x and, with want_codes, the codes are allocated."""
     _need(h, "h", None, 2)
-    T, d = h.shape
-    dev = h.device
-    _shape(gamma, "gamma", torch.float32, (d,), dev)
-    if delta is not None:
-        _shape(delta, "delta", delta.dtype, (T, d), dev)
-    ns = d // group if group else 1
+    T, d = shape = h.shape
+    dev = h.get_device()
+    _on_device(stream, dev)
+    scales_shape = (T, d // group if group else 1)
     if outs is None:
-        outs = dict(x=torch.empty((T, d), dtype=out_dtype, device=dev))
+        outs = dict(x=_out(shape, out_dtype, dev, stream))
         if delta is not None:
-            outs["h"] = torch.empty_like(h)
+            outs["h"] = _out(shape, h.dtype, dev, stream)
         if want_codes:
-            outs["codes"] = torch.empty((T, d), dtype=torch.uint8, device=dev)
-            outs["scales"] = torch.empty((T, ns), dtype=torch.float32, device=dev)
+            outs["codes"] = _out(shape, torch.uint8, dev, stream)
+            outs["scales"] = _out(scales_shape, torch.float32, dev, stream)
     ho, x, codes, scales = outs.get("h"), outs.get("x"), outs.get("codes"), outs.get("scales")
-    _shape(ho, "outs['h']", h.dtype, (T, d), dev)
     if x is not None:
-        _shape(x, "outs['x']", x.dtype, (T, d), dev)
         out_dtype = x.dtype
-    _shape(codes, "outs['codes']", torch.uint8, (T, d), dev)
-    _shape(scales, "outs['scales']", torch.float32, (T, ns), dev)
-    with _On(dev, stream) as s:
-        _check(lib().zmoe_add_rmsnorm(_ptr(h), _dtype_code(h.dtype), _ptr(delta),
-                                      _dtype_code(delta.dtype) if delta is not None else ZMOE_F32, _ptr(gamma),
-                                      float(eps), T, d, _ptr(ho), _ptr(x), _dtype_code(out_dtype), _ptr(codes),
-                                      _ptr(scales), group, s), "zmoe_add_rmsnorm")
+    _call("zmoe_add_rmsnorm", dev, stream, h.data_ptr(), _dtype_code(h.dtype), _at(delta, "delta", None, shape, dev),
+          ZMOE_F32 if delta is None else _dtype_code(delta.dtype), _at(gamma, "gamma", torch.float32, (d,), dev), eps,
+          T, d, _at(ho, "outs['h']", h.dtype, shape, dev), _at(x, "outs['x']", None, shape, dev),
+          _dtype_code(out_dtype), _at(codes, "outs['codes']", torch.uint8, shape, dev),
+          _at(scales, "outs['scales']", torch.float32, scales_shape, dev), group)
     return dict(h=ho, x=x, codes=codes, scales=scales)
 
 
-def _cache_args(k_cache, v_cache, k_scale, v_scale, page_table):
-    """Checks a paged cache; returns (kv dtype code, n_pages, Hkv, page_size, D)."""
+def _cache_dims(k_cache: torch.Tensor):
+    """(kv dtype code, device, n_pages, Hkv, page_size, D) of a paged cache."""
     _need(k_cache, "k_cache", None, 4)
-    dev = k_cache.device
-    if k_cache.dtype not in (torch.bfloat16, torch.uint8):
-        raise TypeError(f"k_cache must be bfloat16 or uint8 (E4M3 codes), got {k_cache.dtype}")
-    _shape(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev)
-    n_pages, Hkv, page_size, D = k_cache.shape
-    _shape(k_scale, "k_scale", torch.float32, (Hkv,), dev)
-    _shape(v_scale, "v_scale", torch.float32, (Hkv,), dev)
-    _need(page_table, "page_table", torch.int32, 2)
-    if page_table.device != dev:
-        raise ValueError(f"page_table is on {page_table.device}, the cache on {dev}")
-    return (ZMOE_E4M3 if k_cache.dtype == torch.uint8 else ZMOE_BF16), n_pages, Hkv, page_size, D
+    if k_cache.dtype is torch.bfloat16:
+        return (ZMOE_BF16, k_cache.get_device(), *k_cache.shape)
+    if k_cache.dtype is torch.uint8:
+        return (ZMOE_E4M3, k_cache.get_device(), *k_cache.shape)
+    raise TypeError(f"k_cache must be bfloat16 or uint8 (E4M3 codes), got {k_cache.dtype}")
 
 
-def _heads(t: torch.Tensor, name: str, T: int, H: int, D: int, dtype, device) -> int:
+def _heads(t: torch.Tensor, name: str, T: int, H: int, D: int, dtype, dev: int) -> int:
     """A [T, H, D] view whose heads are contiguous; returns the elements between its tokens."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (T, H, D):
         raise ValueError(f"{name} must have shape {(T, H, D)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{dev}")
     s0, s1, s2 = t.stride()
     if T and ((D > 1 and s2 != 1) or (H > 1 and s1 != D)):
         raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
@@ -691,8 +694,8 @@ def zmoe_kv_append(k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, k_cache:
     q [T, Hq, D], k, v [T, Hkv, D]: f32 or bf16 views of a packed projection; pos int32 [T]; seq int32 [T] (None:
     token t is sequence t's; negative: padding); k_cache, v_cache [n_pages, Hkv, page_size, D] bf16, or uint8
     E4M3 codes with k_scale, v_scale f32 [Hkv]; page_table int32 [n_seqs, max_pages]; inv_freq f64 [rotary_dim / 2]."""
-    kv, n_pages, Hkv, page_size, D = _cache_args(k_cache, v_cache, k_scale, v_scale, page_table)
-    dev = k_cache.device
+    kv, dev, n_pages, Hkv, page_size, D = _cache_dims(k_cache)
+    _on_device(stream, dev)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must have 3 dims")
     T, dt = k.shape[0], k.dtype
@@ -704,25 +707,20 @@ def zmoe_kv_append(k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, k_cache:
         Hq = q.shape[1]
         qs = _heads(q, "q", T, Hq, D, dt, dev)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+            q_out = _out((T, Hq, D), torch.bfloat16, dev, stream)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _shape(q_out, "q_out", torch.bfloat16, (T, Hq, D), dev)
-    _shape(pos, "pos", torch.int32, (T,), dev)
-    _shape(seq, "seq", torch.int32, (T,), dev)
-    _shape(q_gamma, "q_gamma", torch.float32, (D,), dev)
-    _shape(k_gamma, "k_gamma", torch.float32, (D,), dev)
-    rot = 0
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _shape(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
-    with _On(dev, stream) as s:
-        _check(lib().zmoe_kv_append(_ptr(q), _ptr(k), _ptr(v), _dtype_code(dt), qs, ks, vs, _ptr(seq), _ptr(pos),
-                                    _ptr(inv_freq) if rot else None, rot, int(interleaved), _ptr(q_gamma),
-                                    _ptr(k_gamma), float(eps), T, Hq, Hkv, D, _ptr(q_out), _ptr(k_cache),
-                                    _ptr(v_cache), kv, _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
-                                    page_table.shape[0], page_table.shape[1], n_pages, page_size, s),
-               "zmoe_kv_append")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    table = _at(page_table, "page_table", torch.int32, None, dev)
+    n_seqs, max_pages = page_table.shape
+    _call("zmoe_kv_append", dev, stream, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          _dtype_code(dt), qs, ks, vs, _at(seq, "seq", torch.int32, (T,), dev), _at(pos, "pos", torch.int32, (T,), dev),
+          _at(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev) if rot else None, rot, interleaved,
+          _at(q_gamma, "q_gamma", torch.float32, (D,), dev), _at(k_gamma, "k_gamma", torch.float32, (D,), dev), eps, T,
+          Hq, Hkv, D, _at(q_out, "q_out", torch.bfloat16, (T, Hq, D), dev), k_cache.data_ptr(),
+          _at(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev), kv,
+          _at(k_scale, "k_scale", torch.float32, (Hkv,), dev), _at(v_scale, "v_scale", torch.float32, (Hkv,), dev),
+          table, n_seqs, max_pages, n_pages, page_size)
     return q_out
 
 
@@ -740,32 +738,28 @@ def zmoe_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
 
     page_table int32 [B, max_pages], lens int32 [B]; scale defaults to 1 / sqrt(D); gate f32 [B, Hq]: the output
     times sigmoid(gate); lse f32 [B, Hq] receives the log of the sum of exp(scores)."""
-    kv, n_pages, Hkv, page_size, D = _cache_args(k_cache, v_cache, k_scale, v_scale, page_table)
-    dev = k_cache.device
+    kv, dev, n_pages, Hkv, page_size, D = _cache_dims(k_cache)
+    _on_device(stream, dev)
     _need(q, "q", torch.bfloat16, 3)
     B, Hq, _ = q.shape
-    _shape(q, "q", torch.bfloat16, (B, Hq, D), dev)
-    if page_table.shape[0] != B:
-        raise ValueError(f"page_table has {page_table.shape[0]} rows for {B} sequences")
-    if lens is None:
-        raise ValueError("lens is needed")
-    _shape(lens, "lens", torch.int32, (B,), dev)
-    _shape(gate, "gate", torch.float32, (B, Hq), dev)
-    _shape(lse, "lse", torch.float32, (B, Hq), dev)
+    shape = (B, Hq, D)
+    if page_table is None or lens is None:
+        raise ValueError("page_table and lens are needed")
+    table = _at(page_table, "page_table", torch.int32, None, dev)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must have shape [{B}, max_pages], got {tuple(page_table.shape)}")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=dev)
-    _shape(out, "out", out.dtype, (B, Hq, D), dev)
-    with _On(dev, stream) as s:
-        ws_bytes = zmoe_paged_attention_workspace_size(B, Hq, Hkv, D)
-        if workspace is None:
-            workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
-        _need(workspace, "workspace")
-        _check(lib().zmoe_paged_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), kv, _ptr(k_scale), _ptr(v_scale),
-                                          _ptr(page_table), _ptr(lens), _ptr(gate),
-                                          float(D ** -0.5 if scale is None else scale), B, Hq, Hkv, D,
-                                          page_table.shape[1], n_pages, page_size, _ptr(out), _dtype_code(out.dtype),
-                                          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), s),
-               "zmoe_paged_attention")
+        out = _out(shape, out_dtype, dev, stream)
+    if workspace is None:
+        n = zmoe_paged_attention_workspace_size(B, Hq, Hkv, D)
+        workspace = _out((max(n, 16),), torch.uint8, dev, stream, shared=False)
+    _call("zmoe_paged_attention", dev, stream, _at(q, "q", torch.bfloat16, shape, dev), k_cache.data_ptr(),
+          _at(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev), kv,
+          _at(k_scale, "k_scale", torch.float32, (Hkv,), dev), _at(v_scale, "v_scale", torch.float32, (Hkv,), dev),
+          table, _at(lens, "lens", torch.int32, (B,), dev), _at(gate, "gate", torch.float32, (B, Hq), dev),
+          D ** -0.5 if scale is None else scale, B, Hq, Hkv, D, page_table.shape[1], n_pages, page_size,
+          _at(out, "out", None, shape, dev), _dtype_code(out.dtype), _at(lse, "lse", torch.float32, (B, Hq), dev),
+          _at(workspace, "workspace", None, None, dev), workspace.nbytes)
     return out
 
 
@@ -780,28 +774,23 @@ def zmoe_adjust_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = N
     repetition, presence, frequency: f32 [T]; ``out`` may be ``logits``.  ids: the lowest id of the largest
     adjusted logit, -1 when the mask leaves none."""
     _need(logits, "logits", None, 3)
-    T, N, V = logits.shape
-    dev = logits.device
+    T, N, V = shape = logits.shape
+    dev = logits.get_device()
+    _on_device(stream, dev)
     L = 0
     if history is not None:
         _need(history, "history", torch.int32, 3)
         L = history.shape[1]
-        _shape(history, "history", torch.int32, (T, L, N), dev)
-    _shape(hist_lens, "hist_lens", torch.int32, (T,), dev)
-    for t, name in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
-        _shape(t, name, torch.float32, (T,), dev)
-    _shape(bias, "bias", torch.float32, (N, V), dev)
-    _shape(mask, "mask", torch.int32, (T, N, (V + 31) // 32), dev)
     if out is None:
-        out = torch.empty_like(logits)
+        out = _out(shape, logits.dtype, dev, stream)
     if ids is None:
-        ids = torch.empty((T, N), dtype=torch.int32, device=dev)
-    _shape(out, "out", logits.dtype, (T, N, V), dev)
-    _shape(ids, "ids", torch.int32, (T, N), dev)
-    with _On(dev, stream) as s:
-        _check(lib().zmoe_adjust_logits(_ptr(logits), _dtype_code(logits.dtype), _ptr(history), _ptr(hist_lens),
-                                        _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias), _ptr(mask), T,
-                                        N, V, L, _ptr(out), _ptr(ids), s), "zmoe_adjust_logits")
+        ids = _out((T, N), torch.int32, dev, stream)
+    _call("zmoe_adjust_logits", dev, stream, logits.data_ptr(), _dtype_code(logits.dtype),
+          _at(history, "history", torch.int32, (T, L, N), dev), _at(hist_lens, "hist_lens", torch.int32, (T,), dev),
+          _at(repetition, "repetition", torch.float32, (T,), dev), _at(presence, "presence", torch.float32, (T,), dev),
+          _at(frequency, "frequency", torch.float32, (T,), dev), _at(bias, "bias", torch.float32, (N, V), dev),
+          _at(mask, "mask", torch.int32, (T, N, (V + 31) // 32), dev), T, N, V, L,
+          _at(out, "out", logits.dtype, shape, dev), _at(ids, "ids", torch.int32, (T, N), dev))
     return out, ids
 
 
