@@ -38,147 +38,173 @@ __device__ __forceinline__ float code_scale(float amax) {
   return amax > 0.f ? fmaxf(__fdiv_rn(amax, 448.f), 1.17549435e-38f) : 1.f;
 }
 
-// One row per blockDim.x threads (a multiple of 32), blockDim.y rows per block.
+// One row per blockDim.x threads (a multiple of 32), blockDim.y rows per block at a time.
 template <typename TH, typename TD, typename TX, int CH, int N>
 __global__ void __launch_bounds__(kRowThreads) add_rmsnorm_kernel(AddNormArgs a) {
   constexpr int kVecs = CH / 8;      // vectors of 8 columns a chunk
-  __shared__ float red[2][kRowThreads / 32];
+  constexpr bool kKeep = CH == 16 && N == 1;   // the gains stay in registers from row to row
+  __shared__ float red[2][2][kRowThreads / 32];   // [row parity][sum, largest]
   const int warps_row = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* red_row[2] = {red[0] + threadIdx.y * warps_row, red[1] + threadIdx.y * warps_row};
-  const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const size_t base = static_cast<size_t>(row < a.T ? row : 0) * a.d;
-  const int end = row < a.T ? a.d : 0;   // columns from here on are not there
-  const TH* h = static_cast<const TH*>(a.h) + base;
-  const TD* dl = static_cast<const TD*>(a.delta) + base;
   const int c0 = threadIdx.x * CH, step = blockDim.x * CH;
-  Raw8<TH> raw[N][kVecs];
-  float v[N][kVecs][8];
+  float kept[kKeep ? kVecs : 1][8];
+  auto gains = [&](int c, float* g) {
+    const float4 g0 = __ldg(reinterpret_cast<const float4*>(a.gamma + c));
+    const float4 g1 = __ldg(reinterpret_cast<const float4*>(a.gamma + c) + 1);
+    g[0] = g0.x; g[1] = g0.y; g[2] = g0.z; g[3] = g0.w;
+    g[4] = g1.x; g[5] = g1.y; g[6] = g1.z; g[7] = g1.w;
+  };
+  if (kKeep) {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int c = c0 + i * step + 8 * k;
-      if (c < end) raw[i][k].load(h + c);
-      else raw[i][k].clear();
-    }
-  if (a.delta) {
-    Raw8<TD> add[N][kVecs];
+    for (int k = 0; k < kVecs; ++k)
+      if (c0 + 8 * k < a.d) gains(c0 + 8 * k, kept[k]);
+  }
+  int parity = 0;
+  for (long long first = static_cast<long long>(blockIdx.x) * blockDim.y; first < a.T;
+       first += static_cast<long long>(gridDim.x) * blockDim.y, parity ^= 1) {
+    float* sums = red[parity][0] + threadIdx.y * warps_row;
+    float* tops = red[parity][1] + threadIdx.y * warps_row;
+    const long long row = first + threadIdx.y;
+    const size_t base = static_cast<size_t>(row < a.T ? row : 0) * a.d;
+    const int end = row < a.T ? a.d : 0;   // columns from here on are not there
+    const TH* h = static_cast<const TH*>(a.h) + base;
+    const TD* dl = static_cast<const TD*>(a.delta) + base;
+    Raw8<TH> raw[N][kVecs];
+    float v[N][kVecs][8];
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
         const int c = c0 + i * step + 8 * k;
-        if (c < end) add[i][k].load(dl + c);
-        else add[i][k].clear();
+        if (c < end) raw[i][k].load(h + c);
+        else raw[i][k].clear();
       }
+    if (a.delta) {
+      Raw8<TD> add[N][kVecs];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+      for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k) {
-        float w[8];
-        raw[i][k].get(v[i][k]);
-        add[i][k].get(w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][k][e] += w[e];
-        raw[i][k].put(v[i][k]);
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int k = 0; k < kVecs; ++k) raw[i][k].get(v[i][k]);
-  }
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int c = c0 + i * step + 8 * k;
-      if (a.h_out && c < end) raw[i][k].store(static_cast<TH*>(a.h_out) + base + c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[i][k][e], v[i][k][e], ss);
-    }
-  ss = warp_sum(ss);
-  if (warps_row > 1) {
-    if (lane == 0) red_row[0][warp] = ss;
-    __syncthreads();
-    ss = warp_sum(lane < warps_row ? red_row[0][lane] : 0.f);
-  }
-  const float inv = rsqrtf(fmaf(ss, a.inv_d, a.eps));
-  float amax[N];   // of a chunk
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    amax[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int c = c0 + i * step + 8 * k;
-      if (c < end) {
-        const float4 g0 = __ldg(reinterpret_cast<const float4*>(a.gamma + c));
-        const float4 g1 = __ldg(reinterpret_cast<const float4*>(a.gamma + c) + 1);
-        const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[i][k][e] = v[i][k][e] * inv * g[e];
-          amax[i] = fmaxf(amax[i], fabsf(v[i][k][e]));
+        for (int k = 0; k < kVecs; ++k) {
+          const int c = c0 + i * step + 8 * k;
+          if (c < end) add[i][k].load(dl + c);
+          else add[i][k].clear();
         }
-        if (a.x) store8(static_cast<TX*>(a.x) + base + c, v[i][k]);
-      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+          float w[8];
+          raw[i][k].get(v[i][k]);
+          add[i][k].get(w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][k][e] += w[e];
+          raw[i][k].put(v[i][k]);
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) raw[i][k].get(v[i][k]);
     }
-  }
-  if (!a.codes) return;   // uniform over the grid
-  if (a.group == 0) {
-    float top = amax[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) top = fmaxf(top, amax[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (warps_row > 1) {
-      if (lane == 0) red_row[1][warp] = top;
-      __syncthreads();
-      top = lane < warps_row ? red_row[1][lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    const float s = code_scale(top), r = __frcp_rn(s);
+    float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
         const int c = c0 + i * step + 8 * k;
-        if (c < end)
-          *reinterpret_cast<uint2*>(a.codes + base + c) = make_uint2(e4m3x4(v[i][k], r), e4m3x4(v[i][k] + 4, r));
+        if (a.h_out && c < end) raw[i][k].store(static_cast<TH*>(a.h_out) + base + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(v[i][k][e], v[i][k][e], ss);
       }
-    if (row < a.T && threadIdx.x == 0) a.scales[row] = s;
-  } else {   // 128 columns = 128 / CH neighbouring lanes
+    ss = warp_sum(ss);
+    if (warps_row > 1) {
+      if (lane == 0) sums[warp] = ss;
+      __syncthreads();
+      ss = warp_sum(lane < warps_row ? sums[lane] : 0.f);
+    }
+    const float inv = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+    float amax[N];   // of a chunk
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = c0 + i * step;
-      float top = amax[i];
+      amax[i] = 0.f;
 #pragma unroll
-      for (int o = 64 / CH; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (c < end) {   // d % 128 == 0: whole chunks
-        const float s = code_scale(top), r = __frcp_rn(s);
-        uint32_t w[2 * kVecs];
+      for (int k = 0; k < kVecs; ++k) {
+        const int c = c0 + i * step + 8 * k;
+        if (c < end) {
+          float g[8];
+          if (!kKeep) gains(c, g);
 #pragma unroll
-        for (int k = 0; k < 2 * kVecs; ++k) w[k] = e4m3x4(v[i][k >> 1] + 4 * (k & 1), r);
-        if (kVecs == 2) *reinterpret_cast<uint4*>(a.codes + base + c) = make_uint4(w[0], w[1], w[2 * kVecs - 2], w[2 * kVecs - 1]);
-        else *reinterpret_cast<uint2*>(a.codes + base + c) = make_uint2(w[0], w[1]);
-        if ((c & 127) == 0) a.scales[static_cast<size_t>(row) * (a.d >> 7) + (c >> 7)] = s;
+          for (int e = 0; e < 8; ++e) {
+            v[i][k][e] = v[i][k][e] * inv * (kKeep ? kept[kKeep ? k : 0][e] : g[e]);
+            amax[i] = fmaxf(amax[i], fabsf(v[i][k][e]));
+          }
+          if (a.x) store8(static_cast<TX*>(a.x) + base + c, v[i][k]);
+        }
       }
     }
+    if (!a.codes) {   // uniform over the grid
+      if (!kKeep) return;
+      continue;
+    }
+    if (a.group == 0) {
+      float top = amax[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) top = fmaxf(top, amax[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (warps_row > 1) {
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();
+        top = lane < warps_row ? tops[lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      const float s = code_scale(top), r = __frcp_rn(s);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) {
+          const int c = c0 + i * step + 8 * k;
+          if (c < end)
+            *reinterpret_cast<uint2*>(a.codes + base + c) = make_uint2(e4m3x4(v[i][k], r), e4m3x4(v[i][k] + 4, r));
+        }
+      if (row < a.T && threadIdx.x == 0) a.scales[row] = s;
+    } else {   // 128 columns = 128 / CH neighbouring lanes
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = c0 + i * step;
+        float top = amax[i];
+#pragma unroll
+        for (int o = 64 / CH; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (c < end) {   // d % 128 == 0: whole chunks
+          const float s = code_scale(top), r = __frcp_rn(s);
+          uint32_t w[2 * kVecs];
+#pragma unroll
+          for (int k = 0; k < 2 * kVecs; ++k) w[k] = e4m3x4(v[i][k >> 1] + 4 * (k & 1), r);
+          if (kVecs == 2)
+            *reinterpret_cast<uint4*>(a.codes + base + c) = make_uint4(w[0], w[1], w[2 * kVecs - 2], w[2 * kVecs - 1]);
+          else
+            *reinterpret_cast<uint2*>(a.codes + base + c) = make_uint2(w[0], w[1]);
+          if ((c & 127) == 0) a.scales[static_cast<size_t>(row) * (a.d >> 7) + (c >> 7)] = s;
+        }
+      }
+    }
+    if (!kKeep) return;   // one row a block
   }
 }
 
-// Chunks a thread holds: one as long as 512 threads reach a row's end (N = 1, 2, 4, 8).
+// Chunks a thread holds: one as long as 256 threads reach a row's end.
 template <typename TH, typename TD, typename TX, int CH>
 void launch_row(const AddNormArgs& a, cudaStream_t s) {
   const int chunks = (a.d + CH - 1) / CH;
-  static const int pref = getenv("PREF") ? atoi(getenv("PREF")) : 256;
   int n = 1;
-  while (chunks > pref * n && n * CH < 64) n *= 2;
+  while (chunks > 256 * n && n * CH < 64) n *= 2;
   const int threads = ((chunks + n - 1) / n + 31) / 32 * 32;
   const dim3 block(threads, threads >= 256 ? 1 : 256 / threads);
-  const int grid = (a.T + block.y - 1) / block.y;
+  int grid = (a.T + block.y - 1) / block.y;
+  if (CH == 16 && n == 1) {   // several rows a block (kKeep), as many for each
+    const int most = num_sms() * 4;
+    grid = (grid + (grid + most - 1) / most - 1) / ((grid + most - 1) / most);
+  }
   switch (n) {
     case 1: add_rmsnorm_kernel<TH, TD, TX, CH, 1><<<grid, block, 0, s>>>(a); break;
     case 2: add_rmsnorm_kernel<TH, TD, TX, CH, 2><<<grid, block, 0, s>>>(a); break;

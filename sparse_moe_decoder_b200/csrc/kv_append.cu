@@ -12,10 +12,11 @@
 // that a far position costs no accuracy; the sine and cosine of the fraction are fp32.  They are formed once
 // per token and pair in shared memory and serve every head of the token.
 //
-// Bound by HBM for prompts, by latency for decode steps.  D / 16 lanes carry a head, 16 columns each (eight of each
-// half of its pairs), so a head's sum of squares is a shuffle within its lanes and every access is 16 bytes.  A
-// group of lanes has two heads in flight; the first are asked for before the positions, so a decode step waits for
-// memory twice: for the inputs and indices, then for the page's id.
+// Bound by HBM for prompts, by latency for decode steps.  D / 16 lanes carry a head, so its sum of squares is a
+// shuffle within them.  A lane has two sets of 4 + 4 columns, four pairs each; neighbouring lanes have neighbouring
+// fours, so that a load instruction reads whole lines (with eight neighbouring columns a lane the L1 cache was what
+// bounded f32 prompts).  A group of lanes has two heads in flight; the first are asked for before the positions, so
+// a decode step waits for memory twice: for the inputs and indices, then for the page's id.
 #include "vectors.cuh"
 
 namespace zmoe {
@@ -43,19 +44,41 @@ struct AppendArgs {
   unsigned int* errors;
 };
 
+// Four neighbouring values as they lie in memory, and as fp32.
+template <typename TI>
+struct Raw4;
+template <>
+struct Raw4<float> {
+  float4 r;
+  __device__ __forceinline__ void load(const float* p) { r = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void get(float* v) const { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
+};
+template <>
+struct Raw4<uint16_t> {
+  uint2 r;
+  __device__ __forceinline__ void load(const uint16_t* p) { r = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void get(float* v) const {
+    widen_bf16x2(r.x, v);
+    widen_bf16x2(r.y, v + 2);
+  }
+};
+
+__device__ __forceinline__ void store4(uint16_t* p, const float* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]));
+}
+
 template <typename TI, int D, bool FP8>
 __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 16;                 // lanes of a head
   constexpr int kGroups = kThreads / kLanes;     // heads at a time
-  __shared__ __align__(16) float2 turn[kMaxTokens][kMaxHalf];   // (cos, sin)
+  __shared__ __align__(16) float cosine[kMaxTokens][kMaxHalf], sine[kMaxTokens][kMaxHalf];
   __shared__ long long slot[kMaxTokens];         // cache row of head 0: page * Hkv * page_size + row; -1: skip
   const int t0 = blockIdx.x * a.tokens;
   const int nt = a.T - t0 < a.tokens ? a.T - t0 : a.tokens;
   const int half = a.rot >> 1;
   const int q_heads = a.q ? a.Hq : 0, heads = q_heads + 2 * a.Hkv;
   const int l = threadIdx.x % kLanes;
-  // An item is a head of a token; this lane has its columns c0 .. c0 + 7 and c1 .. c1 + 7.  The heads of the
-  // queries, the keys and the values are numbered one after another.
+  // An item is a head of a token.  The heads of the queries, the keys and the values are numbered one after another.
   struct Item {
     int tt, hd;
     __device__ __forceinline__ void wrap(int heads) {
@@ -65,21 +88,28 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(AppendArgs a) {
       }
     }
   };
+  // Set k of this lane's columns: c0 .. c0 + 3 and c1 .. c1 + 3.
   struct Cols {
-    int kind, hh, c0, c1;   // kind: query, key, value; hh: the head of its kind
+    int c0, c1;
     bool turned;
   };
-  auto cols_of = [&](const Item& it) {
-    Cols x;
-    x.kind = it.hd < q_heads ? 0 : (it.hd < q_heads + a.Hkv ? 1 : 2);
-    x.hh = it.hd - (x.kind == 0 ? 0 : (x.kind == 1 ? q_heads : q_heads + a.Hkv));
-    x.turned = x.kind < 2 && 16 * l < a.rot;
-    const bool apart = x.turned && !a.interleaved;
-    x.c0 = apart ? 8 * l : 16 * l;
-    x.c1 = x.c0 + (apart ? half : 8);
-    return x;
-  };
-  Raw8<TI> raw[kAhead][2];
+  Cols cols[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int j = l + k * kLanes;   // of the head's D / 8 sets, the turned ones first
+    cols[k].turned = 8 * j < a.rot;
+    if (a.interleaved) {
+      cols[k].c0 = 8 * j;
+      cols[k].c1 = 8 * j + 4;
+    } else if (cols[k].turned) {
+      cols[k].c0 = 4 * j;
+      cols[k].c1 = half + 4 * j;
+    } else {
+      cols[k].c0 = half + 4 * j;   // rot + 4 (j - rot / 8)
+      cols[k].c1 = cols[k].c0 + (D - a.rot) / 2;
+    }
+  }
+  Raw4<TI> raw[kAhead][4];
   Item at[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) {
@@ -90,11 +120,16 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(AppendArgs a) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (at[u].tt < nt) {
-        const Cols x = cols_of(at[u]);
-        const TI* src = static_cast<const TI*>(x.kind == 0 ? a.q : (x.kind == 1 ? a.k : a.v)) +
-                        (t0 + at[u].tt) * (x.kind == 0 ? a.q_stride : (x.kind == 1 ? a.k_stride : a.v_stride)) + x.hh * D;
-        raw[u][0].load(src + x.c0);
-        raw[u][1].load(src + x.c1);
+        const int hd = at[u].hd;
+        const TI* src = hd < q_heads ? static_cast<const TI*>(a.q) + (t0 + at[u].tt) * a.q_stride + hd * D
+                        : hd < q_heads + a.Hkv
+                            ? static_cast<const TI*>(a.k) + (t0 + at[u].tt) * a.k_stride + (hd - q_heads) * D
+                            : static_cast<const TI*>(a.v) + (t0 + at[u].tt) * a.v_stride + (hd - q_heads - a.Hkv) * D;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          raw[u][2 * k].load(src + cols[k].c0);
+          raw[u][2 * k + 1].load(src + cols[k].c1);
+        }
       }
     }
   };
@@ -121,74 +156,87 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(AppendArgs a) {
           static_cast<double>(__ldg(a.pos + t0 + t)) * __ldg(a.inv_freq + f) * 0.15915494309189533577;   // 1 / (2 pi)
       float sn, cs;
       sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn, &cs);
-      turn[t][f] = make_float2(cs, sn);
+      cosine[t][f] = cs;
+      sine[t][f] = sn;
     }
   }
   __syncthreads();
   for (int left = nt * heads; left > 0; left -= kAhead * kGroups) {   // every lane takes every round: they shuffle
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int tt = at[u].tt;
-      const Cols it = cols_of(at[u]);
-      float x[16];
-      raw[u][0].get(x);
-      raw[u][1].get(x + 8);
+      const int tt = at[u].tt, hd = at[u].hd;
+      float x[2][8];   // [set][columns c0 .., c1 ..]
+#pragma unroll
+      for (int k = 0; k < 4; ++k) raw[u][k].get(&x[k >> 1][4 * (k & 1)]);
       const long long to = tt < nt ? slot[tt] : -1;
-      const float* gamma = it.kind == 0 ? a.q_gamma : (it.kind == 1 ? a.k_gamma : nullptr);
+      const float* gamma = hd < q_heads ? a.q_gamma : (hd < q_heads + a.Hkv ? a.k_gamma : nullptr);
       if (a.q_gamma || a.k_gamma) {   // the whole warp
         float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int e = 0; e < 16; ++e) ss = fmaf(x[e >> 3][e & 7], x[e >> 3][e & 7], ss);
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (gamma) {
           const float inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float4* gp = reinterpret_cast<const float4*>(gamma + (k ? it.c1 : it.c0));
-            const float4 g0 = __ldg(gp), g1 = __ldg(gp + 1);
+            const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma + cols[k].c0));
+            const float4 g1 = __ldg(reinterpret_cast<const float4*>(gamma + cols[k].c1));
             const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[8 * k + e] = x[8 * k + e] * inv * g[e];
+            for (int e = 0; e < 8; ++e) x[k][e] = x[k][e] * inv * g[e];
           }
         }
       }
       if (to < 0) continue;
-      if (it.turned) {
-        const float4* w = reinterpret_cast<const float4*>(&turn[tt][8 * l]);
+      if (hd < q_heads + a.Hkv) {
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float4 cs = w[e >> 1];   // (cos, sin) of two pairs
-          if (a.interleaved) {
-            const float y0 = x[2 * e], z0 = x[2 * e + 1], y1 = x[2 * e + 2], z1 = x[2 * e + 3];
-            x[2 * e] = y0 * cs.x - z0 * cs.y;
-            x[2 * e + 1] = y0 * cs.y + z0 * cs.x;
-            x[2 * e + 2] = y1 * cs.z - z1 * cs.w;
-            x[2 * e + 3] = y1 * cs.w + z1 * cs.z;
-          } else {
-            const float y0 = x[e], z0 = x[8 + e], y1 = x[e + 1], z1 = x[9 + e];
-            x[e] = y0 * cs.x - z0 * cs.y;
-            x[8 + e] = y0 * cs.y + z0 * cs.x;
-            x[e + 1] = y1 * cs.z - z1 * cs.w;
-            x[9 + e] = y1 * cs.w + z1 * cs.z;
+        for (int k = 0; k < 2; ++k) {
+          if (!cols[k].turned) continue;
+          const float4 c4 = *reinterpret_cast<const float4*>(&cosine[tt][4 * (l + k * kLanes)]);
+          const float4 s4 = *reinterpret_cast<const float4*>(&sine[tt][4 * (l + k * kLanes)]);
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (a.interleaved) {
+              const float y = x[k][2 * e], z = x[k][2 * e + 1];
+              x[k][2 * e] = y * c[e] - z * s[e];
+              x[k][2 * e + 1] = y * s[e] + z * c[e];
+            } else {
+              const float y = x[k][e], z = x[k][4 + e];
+              x[k][e] = y * c[e] - z * s[e];
+              x[k][4 + e] = y * s[e] + z * c[e];
+            }
           }
         }
       }
-      if (it.kind == 0) {
-        uint16_t* dst = a.q_out + (static_cast<size_t>(t0 + tt) * a.Hq + it.hh) * D;
-        store8(dst + it.c0, x);
-        store8(dst + it.c1, x + 8);
+      if (hd < q_heads) {
+        uint16_t* dst = a.q_out + (static_cast<size_t>(t0 + tt) * a.Hq + hd) * D;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          store4(dst + cols[k].c0, x[k]);
+          store4(dst + cols[k].c1, x[k] + 4);
+        }
       } else {
-        const size_t row = static_cast<size_t>(to + static_cast<long long>(it.hh) * a.page_size) * D;
-        void* cache = it.kind == 1 ? a.k_cache : a.v_cache;
+        const bool key = hd < q_heads + a.Hkv;
+        const int hh = hd - q_heads - (key ? 0 : a.Hkv);
+        const size_t row = static_cast<size_t>(to + static_cast<long long>(hh) * a.page_size) * D;
+        void* cache = key ? a.k_cache : a.v_cache;
         if (FP8) {
-          const float rs = __frcp_rn(__ldg((it.kind == 1 ? a.k_scale : a.v_scale) + it.hh));
+          const float rs = __frcp_rn(__ldg((key ? a.k_scale : a.v_scale) + hh));
           uint8_t* dst = static_cast<uint8_t*>(cache) + row;
-          *reinterpret_cast<uint2*>(dst + it.c0) = make_uint2(e4m3x4(x, rs), e4m3x4(x + 4, rs));
-          *reinterpret_cast<uint2*>(dst + it.c1) = make_uint2(e4m3x4(x + 8, rs), e4m3x4(x + 12, rs));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            *reinterpret_cast<uint32_t*>(dst + cols[k].c0) = e4m3x4(x[k], rs);
+            *reinterpret_cast<uint32_t*>(dst + cols[k].c1) = e4m3x4(x[k] + 4, rs);
+          }
         } else {
-          store8(static_cast<uint16_t*>(cache) + row + it.c0, x);
-          store8(static_cast<uint16_t*>(cache) + row + it.c1, x + 8);
+          uint16_t* dst = static_cast<uint16_t*>(cache) + row;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            store4(dst + cols[k].c0, x[k]);
+            store4(dst + cols[k].c1, x[k] + 4);
+          }
         }
       }
     }

@@ -9,18 +9,22 @@
 //
 // Bound by HBM for large vocabularies (logits read once, written once), by latency for one frame.  A row
 // (stream, codebook) is split over a cluster of 1 to 8 CTAs.  Each counts its ids' occurrences in shared memory
-// (16-bit counters, so up to 32768 ids a pass), passes over its logits once, and leaves its best (value, id) in
+// (16-bit counters, so up to 28672 ids a pass), passes over its logits once, and leaves its best (value, id) in
 // the first CTA's shared memory, which takes the largest: no workspace, one launch, and the order in which CTAs
 // finish does not matter.
 //
-// The pass takes four neighbouring logits at an aligned address a thread at a time, two such vectors in flight; the
+// The pass takes a vector of 16 bytes at an aligned address a thread at a time, two such vectors in flight; the
 // first ones are on their way before the counting starts.  Rows of odd length start anywhere in a vector, so a
-// vector's ids begin at 4 i - shift and the counters are laid out by id + shift; the vectors at a row's two ends go
-// element by element, so nothing outside the row is touched.
+// vector's ids begin at E i - shift and the counters are laid out by id + shift; the ids of a row's
+// first and last vectors go one by one, so nothing outside the row is touched.  How the bias lies against the logits is the same for a
+// whole row, and the pass is compiled for each of the four ways (choosing the biases by it in the loop took three
+// instructions an id).
 //
 // The pass leaves out the ids that were counted.  Few as they are, most warps hold one of them, and would take
-// every step of the penalties for it; instead each is listed when its count leaves zero, and a thread of its own
-// takes it.
+// every step of the penalties for it; instead each is listed when its count leaves zero, as the ids at the ends are,
+// and a thread of its own takes it.
+#include <type_traits>
+
 #include "sm100_ptx.cuh"
 #include "vectors.cuh"
 
@@ -31,9 +35,11 @@ using namespace ptx;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 2;          // vectors of four logits in flight a thread
+constexpr int kAhead = 2;          // vectors in flight a thread
+constexpr int kBlocks = 3;         // CTAs an SM
 constexpr int kMaxSplit = 8;       // the portable cluster size
-constexpr int kChunk = 32768;      // ids counted at a time
+constexpr int kChunk = 28672;      // ids counted at a time
+constexpr int kEnds = 32;          // ids at a row's two ends, at most 4 + 7 and 4 + 2 * 7
 constexpr int kMaxHistory = 65535; // what a 16-bit counter holds
 
 struct AdjustArgs {
@@ -47,45 +53,47 @@ struct AdjustArgs {
   int32_t* ids;               // [T, N] or null
   int N, V, L, split;
   int at_once;                // vectors counted at a time
+  int list;                   // ids that can be listed, even
   int same;                   // logits and out lie alike within a vector
   unsigned int* errors;
 };
 
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(uint16_t v) { return bf16_to_f32(v); }
-// Plain loads: `out` may be `logits`.
-__device__ __forceinline__ void load4(const float* p, float* v) {
-  const float4 x = *reinterpret_cast<const float4*>(p);
-  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-}
-__device__ __forceinline__ void load4(const uint16_t* p, float* v) {
-  const uint2 x = *reinterpret_cast<const uint2*>(p);
-  v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xFFFF0000u);
-}
-// Four values rounded to the type (and v to what is stored).
+// A vector of 16 bytes: kE<TL> logits.  Plain loads: `out` may be `logits`.
 template <typename TL>
-struct Out4;
+constexpr int kE = 16 / sizeof(TL);
+
+template <typename TL>
+struct Vec;
 template <>
-struct Out4<float> {
+struct Vec<float> {
   float4 w;
-  __device__ __forceinline__ void round(float* v) { w = make_float4(v[0], v[1], v[2], v[3]); }
+  __device__ __forceinline__ void load(const float* p) { w = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float* v) const { v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w; }
+  __device__ __forceinline__ void round(const float* v) { w = make_float4(v[0], v[1], v[2], v[3]); }
   __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = w; }
-  __device__ __forceinline__ void store_one(float* p, int e) const { *p = e == 0 ? w.x : (e == 1 ? w.y : (e == 2 ? w.z : w.w)); }
 };
 template <>
-struct Out4<uint16_t> {
-  uint2 w;
-  __device__ __forceinline__ void round(float* v) {
-    w = make_uint2(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]));
+struct Vec<uint16_t> {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* v) const {
     widen_bf16x2(w.x, v);
     widen_bf16x2(w.y, v + 2);
+    widen_bf16x2(w.z, v + 4);
+    widen_bf16x2(w.w, v + 6);
   }
-  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = w; }
-  __device__ __forceinline__ void store_one(uint16_t* p, int e) const {
-    *p = static_cast<uint16_t>((e < 2 ? w.x : w.y) >> ((e & 1) * 16));
+  __device__ __forceinline__ void round(const float* v) {
+    w = make_uint4(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]), round_bf16x2(v[4], v[5]), round_bf16x2(v[6], v[7]));
   }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = w; }
 };
+// Of a value that is rounded already.
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = static_cast<uint16_t>(__float_as_uint(v) >> 16); }
+__device__ __forceinline__ float rounded(float, float v) { return v; }
+__device__ __forceinline__ float rounded(uint16_t, float v) { return bf16_to_f32(f32_to_bf16_bits(v)); }
 
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
@@ -99,10 +107,12 @@ __device__ __forceinline__ void take(float& v, uint32_t& i, float w, uint32_t j)
   }
 }
 
-// Four logits from id v on (v may be negative or pass the row's end: `live` bits), their biases and mask bits.
-struct Four {
-  float x[4], b[4];
-  uint32_t live, ok;   // bits of the ids that exist, and that the mask allows
+// The logits of a vector, their biases and mask bits.
+template <typename TL>
+struct Some {
+  Vec<TL> x;
+  float b[kE<TL>];
+  uint32_t ok;   // bits of the ids that the mask allows
 };
 
 template <typename TL>
@@ -110,52 +120,39 @@ struct Row {
   const TL* src;
   const float* bias;
   const uint32_t* mask;
-  int V, turn;   // turn: how far an aligned bias vector begins before the ids' vector
-
-  __device__ __forceinline__ void load(int v, Four& f) const {
-    if (v >= 4 && v + 8 <= V) {   // the bias vectors on both sides lie within the row too
-      load4(src + v, f.x);
-      f.live = 15u;
-      f.ok = 15u;
-      if (mask) f.ok = __funnelshift_r(__ldg(mask + (v >> 5)), __ldg(mask + ((v + 3) >> 5)), v & 31) & 15u;
-      if (bias) {
-        const float4* p = reinterpret_cast<const float4*>(bias + v - turn);
-        const float4 lo = __ldg(p);
-        if (turn == 0) {
-          f.b[0] = lo.x; f.b[1] = lo.y; f.b[2] = lo.z; f.b[3] = lo.w;
-        } else {
-          const float4 hi = __ldg(p + 1);
-          f.b[0] = turn == 1 ? lo.y : (turn == 2 ? lo.z : lo.w);
-          f.b[1] = turn == 1 ? lo.z : (turn == 2 ? lo.w : hi.x);
-          f.b[2] = turn == 1 ? lo.w : (turn == 2 ? hi.x : hi.y);
-          f.b[3] = turn == 1 ? hi.x : (turn == 2 ? hi.y : hi.z);
-        }
-      }
-    } else {
-      f.live = f.ok = 0u;
+  
+  // The vector from id v on; the bias vectors that overlap it lie within the row.  TURN: how far an aligned bias
+  // vector begins before it (-1: no bias).
+  template <int TURN>
+  __device__ __forceinline__ void load(int v, Some<TL>& f) const {
+    constexpr int E = kE<TL>;
+    f.x.load(src + v);
+    f.ok = (1u << E) - 1;
+    if (mask) f.ok &= __funnelshift_r(__ldg(mask + (v >> 5)), __ldg(mask + ((v + E - 1) >> 5)), v & 31);
+    if (TURN >= 0) {
+      const float4* p = reinterpret_cast<const float4*>(bias + v - TURN);
+      float w[E + 4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int id = v + e;
-        f.x[e] = f.b[e] = 0.f;
-        if (id >= 0 && id < V) {
-          f.live |= 1u << e;
-          if (!mask || ((__ldg(mask + (id >> 5)) >> (id & 31)) & 1u)) f.ok |= 1u << e;
-          f.x[e] = as_float(src[id]);
-          if (bias) f.b[e] = __ldg(bias + id);
-        }
+      for (int i = 0; i < (TURN ? E / 4 + 1 : E / 4); ++i) {
+        const float4 q = __ldg(p + i);
+        w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
       }
+#pragma unroll
+      for (int e = 0; e < E; ++e) f.b[e] = w[e + (TURN > 0 ? TURN : 0)];
     }
   }
 };
 
 template <typename TL>
-__global__ void __launch_bounds__(kThreads, 4) adjust_kernel(AdjustArgs a) {
-  extern __shared__ __align__(16) uint32_t counts[];   // 16-bit counters, four a vector; behind them the list
+__global__ void __launch_bounds__(kThreads, kBlocks) adjust_kernel(AdjustArgs a) {
+  extern __shared__ __align__(16) uint32_t counts[];   // 16-bit counters, one an id; behind them the list
   __shared__ int listed;
   __shared__ float best_v[kWarps];
   __shared__ uint32_t best_i[kWarps];
   __shared__ unsigned long long part[kMaxSplit];
-  uint16_t* list = reinterpret_cast<uint16_t*>(counts + 2 * a.at_once);   // counters that are not zero
+  // listed ids, as counters, and their logits
+  uint16_t* list_at = reinterpret_cast<uint16_t*>(counts + (a.history ? kE<TL> / 2 * a.at_once : 0));
+  float* list_x = reinterpret_cast<float*>(list_at + a.list);
   const int rank = blockIdx.x % a.split, row = blockIdx.x / a.split;   // row = t * N + n
   const int t = row / a.N, n = row - t * a.N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -164,15 +161,20 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_kernel(AdjustArgs a) {
   r.src = static_cast<const TL*>(a.logits) + base;
   r.bias = a.bias ? a.bias + static_cast<size_t>(n) * a.V : nullptr;
   r.mask = a.mask ? a.mask + static_cast<size_t>(row) * ((a.V + 31) / 32) : nullptr;
-  r.V = a.V;
-  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(r.src) / sizeof(TL)) & 3;
-  r.turn = static_cast<int>(reinterpret_cast<uintptr_t>(r.bias) / 4 - shift) & 3;
+  constexpr int E = kE<TL>;
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(r.src) / sizeof(TL)) & (E - 1);
+  const int turn = r.bias ? static_cast<int>(reinterpret_cast<uintptr_t>(r.bias) / 4 - shift) & 3 : -1;
   TL* dst = static_cast<TL*>(a.out) + base;
   const bool counted = a.history != nullptr;
   const int32_t* hist = counted ? a.history + static_cast<size_t>(t) * a.L * a.N + n : nullptr;
   // this CTA's vectors
-  const int vecs = (a.V + shift + 3) / 4, per = (vecs + a.split - 1) / a.split;
+  const int vecs = (a.V + shift + E - 1) / E, per = (vecs + a.split - 1) / a.split;
   const int i_begin = rank * per, i_end = i_begin + per < vecs ? i_begin + per : vecs;
+  // the ids [0, low_end) and [high_begin, V) of the row go one by one, the vectors between them whole
+  const int i_low = (4 + shift + E - 1) / E, i_high = a.V + shift >= E + 4 ? (a.V + shift - 4) / E : 0;
+  const int low_end = E * i_low - shift < a.V ? E * i_low - shift : a.V;
+  const int high_begin = E * i_high - shift > low_end ? E * i_high - shift : low_end;
+  const int i_first = i_begin > i_low ? i_begin : i_low, i_last = i_end < i_high ? i_end : i_high;
   // all that the first counts and vectors need is asked for at once
   int32_t early[2];
 #pragma unroll
@@ -187,123 +189,173 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_kernel(AdjustArgs a) {
   }
   const float rep = a.repetition ? __ldg(a.repetition + t) : 1.f, pre = a.presence ? __ldg(a.presence + t) : 0.f,
               frq = a.frequency ? __ldg(a.frequency + t) : 0.f;
-  Four f[kAhead];
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
-    const int i = i_begin + static_cast<int>(threadIdx.x) + u * kThreads;
-    if (i < i_end) r.load(4 * i - shift, f[u]);
-  }
-  float bv = __int_as_float(0xff800000);   // the best of this thread so far
-  uint32_t bi = 0xFFFFFFFFu, low = 0xFFFFFFFFu;   // its id; the lowest id that may win at all
-  for (int c0 = i_begin; c0 < i_end; c0 += a.at_once) {
-    const int c1 = i_end - c0 < a.at_once ? i_end : c0 + a.at_once;
-    const int first = 4 * c0 - shift;   // the id of counter 0
-    // the id of a listed counter, what is known of it, and what becomes of it
-    float lx = 0.f, lb = 0.f;
-    bool lok = true;
-    auto ask = [&](int id) {
-      lx = as_float(r.src[id]);
-      if (r.bias) lb = __ldg(r.bias + id);
-      if (r.mask) lok = (__ldg(r.mask + (id >> 5)) >> (id & 31)) & 1u;
-    };
-    auto settle = [&](int at) {
-      const uint32_t c = (counts[at >> 1] >> ((at & 1) * 16)) & 0xFFFFu;
-      float x[4] = {lx, 0.f, 0.f, 0.f};
-      if (a.repetition) x[0] = x[0] > 0.f ? __fdiv_rn(x[0], rep) : __fmul_rn(x[0], rep);
-      if (a.frequency) x[0] = __fsub_rn(x[0], __fmul_rn(frq, static_cast<float>(c)));
-      if (a.presence) x[0] = __fsub_rn(x[0], pre);
-      if (r.bias) x[0] = __fadd_rn(x[0], lb);
-      if (!lok) x[0] = __int_as_float(0xff800000);
-      Out4<TL> o;
-      o.round(x);
-      o.store_one(dst + first + at, 0);
-      if (lok && x[0] == x[0]) take(bv, bi, x[0], static_cast<uint32_t>(first + at));
-    };
-    int mine = -1;
-    if (counted) {
-      __syncthreads();   // the previous chunk's counts are read
-      for (int i = threadIdx.x; i < c1 - c0; i += kThreads) reinterpret_cast<uint2*>(counts)[i] = make_uint2(0u, 0u);
-      if (threadIdx.x == 0) listed = 0;
-      __syncthreads();
-      auto count = [&](int32_t id) {
-        const unsigned at = static_cast<unsigned>(id - first);
-        if (id >= 0 && id < a.V && at < 4u * (c1 - c0)) {
-          const uint32_t was = atomicAdd(&counts[at >> 1], 1u << ((at & 1) * 16));
-          if (((was >> ((at & 1) * 16)) & 0xFFFFu) == 0) list[atomicAdd(&listed, 1)] = static_cast<uint16_t>(at);
-        }
-        if (id >= a.V && rank == 0 && c0 == 0) record_device_error(a.errors);   // a negative id is no id
-      };
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (static_cast<int>(threadIdx.x) + u * kThreads < len) count(early[u]);
-#pragma unroll 4
-      for (int i = threadIdx.x + 2 * kThreads; i < len; i += kThreads) count(__ldg(hist + static_cast<size_t>(i) * a.N));
-      __syncthreads();
-      if (static_cast<int>(threadIdx.x) < listed) {
-        mine = list[threadIdx.x];
-        ask(first + mine);
-      }
-    }
-    for (int at = c0; at < c1; at += kAhead * kThreads) {
+  const float none = __int_as_float(0xff800000);
+  float bv = none;             // the best of this thread so far
+  uint32_t bi = 0xFFFFFFFFu;   // its id
+  auto pass = [&](auto turn_c) {
+    constexpr int TURN = decltype(turn_c)::value;
+    Some<TL> f[kAhead];
+    auto fetch = [&](int at) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int i = at + static_cast<int>(threadIdx.x) + u * kThreads, v = 4 * i - shift;
-        if (i >= c1) continue;
-        uint32_t live = f[u].live, ok = f[u].ok;
-        if (counted) {
-          const uint2 c = reinterpret_cast<const uint2*>(counts)[i - c0];
-          if (c.x | c.y) {
-            const uint32_t rest = ((c.x & 0xFFFFu) == 0 ? 1u : 0u) | (c.x < 0x10000u ? 2u : 0u) |
-                                  ((c.y & 0xFFFFu) == 0 ? 4u : 0u) | (c.y < 0x10000u ? 8u : 0u);
-            live &= rest;
-            ok &= rest;
+        const int i = at + static_cast<int>(threadIdx.x) + u * kThreads;
+        if (i < i_last) r.template load<TURN>(E * i - shift, f[u]);
+      }
+    };
+    fetch(i_first);
+    for (int c0 = i_begin; c0 < i_end; c0 += a.at_once) {
+      const int c1 = i_end - c0 < a.at_once ? i_end : c0 + a.at_once;
+      const int first = E * c0 - shift;   // the id of counter 0
+      const unsigned span = static_cast<unsigned>(E * (c1 - c0));
+      __syncthreads();   // the previous chunk's counts and list are read
+      if (counted) {
+        for (int i = threadIdx.x; i < (c1 - c0) * E / 4; i += kThreads)
+          reinterpret_cast<uint2*>(counts)[i] = make_uint2(0u, 0u);
+      }
+      if (threadIdx.x == 0) listed = 0;
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < low_end + a.V - high_begin) {
+        const int id = static_cast<int>(threadIdx.x) < low_end ? threadIdx.x : high_begin + threadIdx.x - low_end;
+        const unsigned at = static_cast<unsigned>(id - first);
+        if (at < span) list_at[atomicAdd(&listed, 1)] = static_cast<uint16_t>(at);
+      }
+      if (counted) {
+        auto count = [&](int32_t id) {
+          const unsigned at = static_cast<unsigned>(id - first);
+          if (id >= 0 && at < span && id < a.V) {
+            const uint32_t was = atomicAdd(&counts[at >> 1], 1u << ((at & 1) * 16));
+            if (((was >> ((at & 1) * 16)) & 0xFFFFu) == 0 && id >= low_end && id < high_begin)
+              list_at[atomicAdd(&listed, 1)] = static_cast<uint16_t>(at);
           }
-        }
-        float x[4];
+          if (id >= a.V && rank == 0 && c0 == 0) record_device_error(a.errors);   // a negative id is no id
+        };
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = r.bias ? __fadd_rn(f[u].x[e], f[u].b[e]) : f[u].x[e];
-          if (!((ok >> e) & 1u)) x[e] = __int_as_float(0xff800000);
-        }
-        Out4<TL> o;
-        o.round(x);
-        if (live == 15u && a.same) {
-          o.store(dst + v);
+        for (int u = 0; u < 2; ++u)
+          if (static_cast<int>(threadIdx.x) + u * kThreads < len) count(early[u]);
+#pragma unroll 4
+        for (int i = threadIdx.x + 2 * kThreads; i < len; i += kThreads) count(__ldg(hist + static_cast<size_t>(i) * a.N));
+      }
+      __syncthreads();
+      // the listed logits are read before the pass writes anything, for `out` may be `logits`
+      const int n_listed = listed;
+      float lb = 0.f;
+      bool lok = true;
+      auto ask = [&](int i) {   // the bias and the mask of a listed id
+        const int id = first + list_at[i];
+        if (TURN >= 0) lb = __ldg(r.bias + id);
+        if (r.mask) lok = (__ldg(r.mask + (id >> 5)) >> (id & 31)) & 1u;
+      };
+#pragma unroll 2
+      for (int i = threadIdx.x; i < n_listed; i += kThreads) list_x[i] = as_float(r.src[first + list_at[i]]);
+      if (static_cast<int>(threadIdx.x) < n_listed) ask(threadIdx.x);
+      if (n_listed) __syncthreads();
+      const int s0 = c0 > i_first ? c0 : i_first, s1 = c1 < i_last ? c1 : i_last;
+      int best_at = -1, allowed_at = -1;   // the vector of this chunk's best, and the first that allows an id
+      Vec<TL> best;
+      auto rest_of = [&](int i) -> uint32_t {   // bits of the vector's ids that are not listed
+        uint32_t c[E / 2], any = 0, rest = (1u << E) - 1;
+        if (E == 8) {
+          const uint4 q = reinterpret_cast<const uint4*>(counts)[i - c0];
+          c[0] = q.x; c[1] = q.y; c[E / 2 - 2] = q.z; c[E / 2 - 1] = q.w;
         } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if ((live >> e) & 1u) o.store_one(dst + v + e, e);
+          const uint2 q = reinterpret_cast<const uint2*>(counts)[i - c0];
+          c[0] = q.x; c[1] = q.y;
         }
-        // Ids ascend along a thread's way, so only a larger value replaces its best one; NaN never does, nor does
-        // the -inf of an id that is left out.  An allowed -inf counts when nothing larger comes.
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (x[e] > bv) {
-            bv = x[e];
-            bi = static_cast<uint32_t>(v + e);
+        for (int k = 0; k < E / 2; ++k) any |= c[k];
+        if (any) {
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) {
+            if (c[k] & 0xFFFFu) rest &= ~(1u << (2 * k));
+            if (c[k] >> 16) rest &= ~(2u << (2 * k));
           }
-        if (low == 0xFFFFFFFFu && ok) {
+        }
+        return rest;
+      };
+      for (int at = s0; at < s1; at += kAhead * kThreads) {
 #pragma unroll
-          for (int e = 3; e >= 0; --e)
-            if (((ok >> e) & 1u) && x[e] == x[e]) low = static_cast<uint32_t>(v + e);
+        for (int u = 0; u < kAhead; ++u) {
+          const int i = at + static_cast<int>(threadIdx.x) + u * kThreads, v = E * i - shift;
+          if (i >= s1) continue;
+          uint32_t ok = f[u].ok;
+          if (counted) ok &= rest_of(i);
+          float x[E];
+          f[u].x.get(x);
+          if (TURN >= 0) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = __fadd_rn(x[e], f[u].b[e]);
+          }
+          if (ok != (1u << E) - 1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (!((ok >> e) & 1u)) x[e] = none;
+          }
+          Vec<TL> o;
+          o.round(x);
+          // listed ids get their value behind the pass
+          if (a.same) {
+            o.store(dst + v);
+          } else {
+            o.get(x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) store1(dst + v + e, x[e]);
+          }
+          // Vectors ascend along a thread's way, so only a larger value replaces the best one; NaN never does, nor
+          // does the -inf of an id that is left out.  Rounding keeps the order.
+          float top = x[0];
+#pragma unroll
+          for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
+          top = rounded(TL(), top);
+          if (top > bv) {
+            bv = top;
+            best_at = i;
+            best = o;
+          }
+          if (allowed_at < 0 && ok) allowed_at = i;
+        }
+        fetch(at + kAhead * kThreads < s1 ? at + kAhead * kThreads : s1);   // of the next chunk too
+      }
+      if (best_at >= 0) {
+        float x[E];
+        best.get(x);
+#pragma unroll
+        for (int e = E - 1; e >= 0; --e)
+          if (x[e] == bv) bi = static_cast<uint32_t>(E * best_at - shift + e);
+      } else if (bi == 0xFFFFFFFFu && allowed_at >= 0) {   // all that is allowed here is -inf or NaN: the first -inf
+        for (int i = allowed_at; i < s1 && bi == 0xFFFFFFFFu; i += kThreads) {
+          const int v = E * i - shift;
+          uint32_t ok = counted ? rest_of(i) : (1u << E) - 1;
+          if (r.mask) ok &= __funnelshift_r(r.mask[v >> 5], r.mask[(v + E - 1) >> 5], v & 31);
+          for (int e = E - 1; e >= 0; --e)
+            if (((ok >> e) & 1u) && as_float(dst[v + e]) == none) bi = static_cast<uint32_t>(v + e);
         }
       }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {   // the next vectors, of the next chunk too
-        const int i = (at + kAhead * kThreads < c1 ? at + kAhead * kThreads : c1) + static_cast<int>(threadIdx.x) + u * kThreads;
-        if (i < i_end) r.load(4 * i - shift, f[u]);
+      if (n_listed) __syncthreads();   // the pass's vectors are written
+      for (int i = threadIdx.x; i < n_listed; i += kThreads) {
+        if (i >= kThreads) ask(i);
+        const int at = list_at[i], id = first + at;
+        const uint32_t c = counted ? (counts[at >> 1] >> ((at & 1) * 16)) & 0xFFFFu : 0u;
+        float x = list_x[i];
+        if (c) {
+          if (a.repetition) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+          if (a.frequency) x = __fsub_rn(x, __fmul_rn(frq, static_cast<float>(c)));
+          if (a.presence) x = __fsub_rn(x, pre);
+        }
+        if (TURN >= 0) x = __fadd_rn(x, lb);
+        x = lok ? rounded(TL(), x) : none;
+        store1(dst + id, x);
+        if (lok && x == x) take(bv, bi, x, static_cast<uint32_t>(id));
       }
     }
-    if (mine >= 0) {
-      settle(mine);
-      for (int i = threadIdx.x + kThreads; i < listed; i += kThreads) {
-        ask(first + list[i]);
-        settle(list[i]);
-      }
-    }
+  };
+  switch (turn) {   // the same for the whole CTA
+    case -1: pass(std::integral_constant<int, -1>()); break;
+    case 0: pass(std::integral_constant<int, 0>()); break;
+    case 1: pass(std::integral_constant<int, 1>()); break;
+    case 2: pass(std::integral_constant<int, 2>()); break;
+    default: pass(std::integral_constant<int, 3>()); break;
   }
   if (!a.ids) return;   // uniform over the grid
-  take(bv, bi, __int_as_float(0xff800000), low);
   // the first CTA of the cluster runs before any other writes to it
   if (a.split > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 #pragma unroll
@@ -342,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_kernel(AdjustArgs a) {
 template <typename TL>
 zmoe_status launch(const AdjustArgs& a, int rows, size_t smem, cudaStream_t s) {
   if (smem > 40 * 1024 && cudaFuncSetAttribute(adjust_kernel<TL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kChunk * 4) != cudaSuccess)
+                                               kChunk * 8 + kEnds * 6) != cudaSuccess)
     return check_launch("zmoe_adjust_logits: shared memory attribute");
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(rows) * a.split);
@@ -395,16 +447,19 @@ extern "C" zmoe_status zmoe_adjust_logits(const void* logits, zmoe_dtype dtype, 
   a.bias = bias; a.mask = mask; a.ids = ids;
   a.N = N; a.V = V; a.L = L;
   a.errors = device_error_counter();
-  const int low = dtype == ZMOE_BF16 ? 7 : 15;   // a vector's bytes less one
-  a.same = ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(out)) & low) == 0;
-  // enough CTAs for the machine, but at least 2048 ids each
+  a.same = ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+  // as many CTAs as run at once, with at least 2048 ids each
   int split = 1;
-  while (split < kMaxSplit && rows * split < 8LL * num_sms() && V / (2 * split) >= 2048) split *= 2;
+  while (split < kMaxSplit && rows * split * 2 <= static_cast<long long>(kBlocks) * num_sms() && V / (2 * split) >= 2048)
+    split *= 2;
   a.split = split;
-  const int vecs = ((V + 6) / 4 + split - 1) / split;
-  a.at_once = vecs < kChunk / 4 ? vecs : kChunk / 4;
-  const int most = L < 4 * a.at_once ? L : 4 * a.at_once;   // ids that can be listed
-  const size_t smem = a.history ? static_cast<size_t>(a.at_once) * 8 + static_cast<size_t>(most) * 2 : 0;
+  const int E = dtype == ZMOE_BF16 ? 8 : 4;
+  const int vecs = ((V + 2 * E - 2) / E + split - 1) / split;
+  const int chunks = (vecs + kChunk / E - 1) / (kChunk / E);
+  a.at_once = (vecs + chunks - 1) / chunks;
+  a.list = kEnds;
+  if (a.history) a.list += ((L < E * a.at_once ? L : E * a.at_once) + 1) & ~1;
+  const size_t smem = (a.history ? static_cast<size_t>(a.at_once) * E * 2 : 0) + static_cast<size_t>(a.list) * 6;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dtype == ZMOE_BF16 ? launch<uint16_t>(a, static_cast<int>(rows), smem, s)
                             : launch<float>(a, static_cast<int>(rows), smem, s);
