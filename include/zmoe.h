@@ -495,7 +495,7 @@ ZMOE_API size_t zmoe_paged_attention_workspace_size(int B, int Hq, int Hkv, int 
  *   read but never used, NaN included.
  *   fp32 accumulation; the results do not depend on the order in which CTAs finish.  Two launches on `stream`.  The
  *   workspace (16-byte aligned) belongs to one call at a time: calls that may overlap need one each.
- *   Hq % Hkv == 0, D = 64 or 128 (else ZMOE_ERR_UNSUPPORTED), page_size % 16 == 0, n_pages * Hkv * page_size < 2^32 - 1.
+ *   Hq % Hkv == 0, D = 64 or 128 (else ZMOE_ERR_UNSUPPORTED), page_size % 16 == 0, n_pages * Hkv * page_size < 2^31 - 1.
  */
 ZMOE_API zmoe_status zmoe_paged_attention(const void* q, const void* k_cache, const void* v_cache, zmoe_dtype kv_dtype,
                                           const float* k_scale, const float* v_scale, const int32_t* page_table,

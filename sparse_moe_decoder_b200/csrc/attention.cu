@@ -6,36 +6,45 @@
 //   out_i = sigmoid(gate_i) o_i                                               (o = 0, lse = -inf when n = 0)
 //
 // Bound by HBM: every cached key and value is read once (per 8 or 16 query heads of a group).  A warp takes 16
-// tokens at a time, which lie in one page, straight into registers: no shared memory, no barrier in the loop.
+// tokens at a time, which lie in one page.  Their keys, then their values, come by TMA into the warp's own ring in
+// shared memory (128-byte swizzle, an mbarrier a slot), 12 to 24 KB ahead of the products; 16 warps an SM keep
+// 192 KB in flight, and no warp waits for another.
 //   scores  S = Q K^T:      m16n8k16, 16 rows of query heads (8 or 16 in use), 8 tokens, 16 columns;
 //   output  O^T = V^T P^T:  m16n8k16, 16 columns of V, 8 query heads, 16 tokens.
+// (A tcgen05 product has at least 64 rows, of which a group's heads would fill 4 or 8, and its accumulator lies in
+// tensor memory, from where the softmax would have to fetch it; the warp's product leaves S in registers.)
 // The contraction index of a tensor-core product may be permuted as long as both operands agree, so each lane's
-// share of a key row is 16 contiguous bytes, and each lane's share of the output is D / 8 contiguous columns.
-// S leaves the first product in the layout that the second takes P^T in.  The maximum and the sum of the
-// softmax run along in registers.
-//
-// The loads of the next 16 keys are issued as soon as S is formed, those of the next values as soon as O is.
+// share of a key row is 16-byte chunks, each lane's share of the output is 8 contiguous columns, and the swizzle
+// keeps both free of bank conflicts.  S leaves the first product in the layout that the second takes P^T in.  The
+// maximum and the sum of the softmax run along in registers.
 //
 // Work is split over the cache's length: the (sequence, group, 16-token tile) triples are one line of tiles,
-// cut into equal pieces, one a warp, so that ragged lengths balance.  A warp writes the groups that lie within
-// its piece; of a group that is cut it leaves (maximum, sum, O) in the workspace, and a second kernel, launched
-// to start early (programmatic dependent launch), joins them in a fixed order.
+// cut into equal pieces, one a warp, so that ragged lengths balance; the ring runs ahead over the ends of
+// sequences.  A warp writes the groups that lie within its piece; of a group that is cut it leaves (maximum, sum, O)
+// in the workspace, and a second kernel, launched to start early (programmatic dependent launch), joins them in a
+// fixed order.
 //
 // P is split into two 16-bit terms, P = P_hi + P_lo (the second product runs twice): one bf16 term alone would
-// cost 2^-9 of every weight.  An infinite value times a P_lo of zero or of the other sign would be NaN where the
-// formula has an infinity, so a piece whose output holds a NaN is passed over once more with the second term
-// leaving infinities out.  An 8-bit cache is expanded to f16, exactly; its queries are scaled by a power of
-// two per head to use f16's range, and so is P.
+// cost 2^-9 of every weight.  P_hi is cut, not rounded, so that P_lo is never negative, and P_lo is at least 2^-126
+// where P is not 0: an infinite value then meets two positive weights and stays an infinity, as in the formula.
+// An 8-bit cache is expanded to f16, exactly; its queries are scaled by a power of two per head to use f16's range,
+// and so is P.
 #include "sm100_ptx.cuh"
+#include "vectors.cuh"
 
 namespace zmoe {
+
+unsigned int* device_timeout_counter();
+
 namespace {
 
 using namespace ptx;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kJoinThreads = 256;
 constexpr int kMaxWarpsPerSm = 16;
+constexpr uint64_t kWaitNs = 2000000000ull;   // a wait for a copy gives up after this
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -52,7 +61,7 @@ struct AttnArgs {
   float* lse;             // [B, Hq] or null
   float* parts;           // [warps][2] of {m[H], l[H], O[H][D]}, H = 8 HT
   int warps;              // warps of the first kernel
-  unsigned int* errors;
+  unsigned int *errors, *timeouts;
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -103,6 +112,7 @@ struct Pieces {
 };
 
 // Exclusive prefix over the block's threads of `mine`; every thread receives the total.
+template <int WARPS>
 __device__ __forceinline__ long long block_prefix(long long mine, long long* scratch, long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long inc = mine;
@@ -116,7 +126,7 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long* scr
   long long before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
@@ -128,55 +138,44 @@ __host__ __device__ constexpr int part_floats() {
   return 8 * HT * (D + 2);
 }
 
-// The types of an 8-bit or a bf16 cache: 16-byte vectors of a lane per key row, and bytes of a lane per value row.
-template <int D, bool FP8>
+// How tiles of an 8-bit or a bf16 cache are read.  A tile's rows lie in shared memory as boxes of 128-byte lines
+// (two boxes of half rows where a row has 256 bytes, two rows a line where it has 64), each line's 16-byte chunks
+// exchanged by the line's number.
+template <int D, bool FP8, int HT>
 struct Lay {
   static constexpr int esz = FP8 ? 1 : 2;
-  static constexpr int kvecs = D * esz / 64;       // 16-byte vectors of a key row per lane (4 lanes a row)
-  static constexpr int vwords = D * esz / 32;      // 32-bit words of a value row per lane (8 lanes a row)
+  static constexpr int row = D * esz;              // bytes
+  static constexpr int kvecs = row / 64;           // 16-byte vectors of a key row per lane (4 lanes a row)
+  static constexpr int vwords = row / 32;          // 32-bit words of a value row per lane (8 lanes a row)
   static constexpr int steps = D / 16;             // 16-column steps of the first product
   static constexpr int mt = D / 16;                // 16-column tiles of the output
+  static constexpr int slot = 16 * row;            // bytes of a tile's keys or values
+  static constexpr int blocks = HT == 1 ? 4 : 2;   // CTAs an SM: 128 or 255 registers a thread
+  static constexpr int ring = HT == 1 ? 12288 : 24576;   // bytes a warp
+  static constexpr int slots = ring / slot < 12 ? ring / slot : 12;
+  static constexpr int smem = kWarps * slots * slot + 1024;   // the ring starts on 1024 bytes
+  static_assert(slots >= 2 && slot % 1024 == 0, "whole swizzle atoms");
+
+  // Chunk c of lane j's share of a key row, in 16-byte chunks of the row.
+  __device__ __forceinline__ static int k_chunk(int c, int j) { return row >= 128 ? (c >> 1) * 8 + 2 * j + (c & 1) : j; }
+  // Byte `at` of token r's row within the slot.
+  __device__ __forceinline__ static uint32_t place(int r, int at) {
+    const uint32_t x = row == 256 ? static_cast<uint32_t>((at >> 7) * 2048 + r * 128 + (at & 127))
+                                  : static_cast<uint32_t>(r * row + at);
+    return x ^ (((x >> 7) & 7u) << 4);
+  }
 };
 
-template <int D, bool FP8>
-__device__ __forceinline__ void load_k(const unsigned char* rows, int g, int j, uint4 (&k)[2][Lay<D, FP8>::kvecs]) {
-  using L = Lay<D, FP8>;
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int c = 0; c < L::kvecs; ++c)
-      k[r][c] = ldg_stream(rows + static_cast<size_t>(g + 8 * r) * (D * L::esz) + c * 64 + j * 16);
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(p));
+  return r;
 }
 
-template <int D, bool FP8>
-__device__ __forceinline__ void load_v(const unsigned char* rows, int g, int j, uint32_t (&v)[4][Lay<D, FP8>::vwords]) {
-  using L = Lay<D, FP8>;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int tok = 2 * j + (r & 1) + 8 * (r >> 1);
-    const unsigned char* p = rows + static_cast<size_t>(tok) * (D * L::esz);
-    if (L::vwords == 2) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p + g * 8));
-      v[r][0] = w.x;
-      v[r][1] = w.y;
-    } else {
-#pragma unroll
-      for (int c = 0; c < L::vwords / 4; ++c) {
-        const uint4 w = ldg_stream(p + c * 128 + g * 16);
-        v[r][4 * c] = w.x;
-        v[r][4 * c + 1] = w.y;
-        v[r][4 * c + 2] = w.z;
-        v[r][4 * c + 3] = w.w;
-      }
-    }
-  }
-}
-
-// Two bf16 values, infinities and NaN replaced by 0.
-__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t x) {
-  if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-  if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
-  return x;
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(p));
+  return r;
 }
 
 // The column of V that word w's lower half (bf16) or first byte (8 bits) of lane group g holds.
@@ -202,16 +201,25 @@ __device__ __forceinline__ float gate_of(const AttnArgs& a, int b, int head) {
 }
 
 template <int D, bool FP8, int HT, typename TO>
-__global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArgs a) {
-  using L = Lay<D, FP8>;
+__global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
+    attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a) {
+  using L = Lay<D, FP8, HT>;
   constexpr int H = 8 * HT;
   constexpr float kPScale = FP8 ? 32768.f : 1.f;   // f16 holds P in [0, 2^15]: weights down to 2^-39 survive
+  extern __shared__ unsigned char ring_raw[];
+  __shared__ uint64_t bars[kWarps][L::slots];
   __shared__ long long scan[kWarps];
   __shared__ int at_b[kWarps];
   __shared__ long long at_off[kWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
   const int units = a.Hkv * a.gtiles;
+  uint64_t* bar = bars[warp];
+  const uint32_t ring = ((smem_u32(ring_raw) + 1023u) & ~1023u) + static_cast<uint32_t>(warp * L::slots * L::slot);
+  if (lane == 0) {
+    for (int i = 0; i < L::slots; ++i) mbar_init(bar + i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
+  }
   // the line of tiles: sequence by sequence, in each the groups, in each the tiles
   const int per = (a.B + kThreads - 1) / kThreads, b_lo = threadIdx.x * per;
   const int b_hi = b_lo + per < a.B ? b_lo + per : a.B;
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
       record_device_error(a.errors);
   }
   long long total;
-  const long long pre = block_prefix(mine, scan, total);
+  const long long pre = block_prefix<kWarps>(mine, scan, total);
   if (total == 0) return;
   const Pieces pieces(total, a.warps);
 #pragma unroll
@@ -243,12 +251,99 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
   __syncthreads();
   const long long gw = static_cast<long long>(blockIdx.x) * kWarps + warp;
   if (gw >= pieces.count) return;
-  const long long x0 = pieces.start(gw), x1 = pieces.start(gw + 1);
+  const int piece = static_cast<int>(pieces.start(gw + 1) - pieces.start(gw));   // tiles; 2^31 of them would take hours
   int b = at_b[warp], n = seq_len(a, b), nt = tiles_of(n);
-  int u = static_cast<int>(at_off[warp] / nt), tile = static_cast<int>(at_off[warp] - static_cast<long long>(u) * nt);
+  int u = static_cast<int>(divide(at_off[warp], nt)), tile = static_cast<int>(at_off[warp] - static_cast<long long>(u) * nt);
+
+  // The feeder runs ahead of the products: keys and values of one tile after another, each into the next slot.
   const int tpp = a.page_size >> 4;   // tiles per page
-  for (long long x = x0; x < x1;) {
-    const int t_end = x1 - x < nt - tile ? tile + static_cast<int>(x1 - x) : nt;
+  int f_b = b, f_u = u, f_tile = tile, f_nt = nt, f_win = tile, f_slot = 0;
+  int f_left = piece;                 // tiles to feed
+  bool f_key = true;
+  uint32_t f_row = 0, f_have = 0;     // the tile's cache row; bit t & 31: the t-th tile of the piece has a page
+  int f_count = 0;
+  // cache rows of the 32 tiles from f_win on (lane i: tile f_win + i); 0xffffffff: no page
+  auto rows_from = [&](int win) -> uint32_t {
+    const int t = win + lane;
+    uint32_t r = 0xFFFFFFFFu;
+    if (t < f_nt && t - f_tile < f_left) {
+      const int col = t / tpp;
+      const int pid = __ldg(a.table + static_cast<size_t>(f_b) * a.max_pages + col);
+      if (pid >= 0 && pid < a.n_pages)
+        r = (static_cast<uint32_t>(pid) * a.Hkv + f_u / a.gtiles) * a.page_size + static_cast<uint32_t>(t - col * tpp) * 16u;
+      else if (f_u == 0 && (t == f_tile || t == col * tpp))
+        record_device_error(a.errors);
+    }
+    return r;
+  };
+  uint32_t f_rows = rows_from(f_win);
+  auto feed = [&]() {
+    if (f_left == 0) return;
+    if (f_key) {
+      const uint32_t r = __shfl_sync(0xffffffffu, f_rows, f_tile - f_win);
+      const bool have = r != 0xFFFFFFFFu;
+      f_row = have ? r : 0u;   // any row in its place: its tokens do not count
+      const uint32_t bit = 1u << (f_count & 31);
+      f_have = have ? f_have | bit : f_have & ~bit;
+      ++f_count;
+    }
+    if (lane == 0) {
+      uint64_t* full = bar + f_slot;
+      const CUtensorMap* map = f_key ? &kmap : &vmap;
+      const uint32_t dst = ring + f_slot * L::slot;
+      mbar_expect_tx(full, L::slot);
+      const int line = static_cast<int>(L::row == 64 ? f_row >> 1 : f_row);
+#pragma unroll
+      for (int half = 0; half < (L::row == 256 ? 2 : 1); ++half)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                dst + half * 2048),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(full)), "r"(half * 128), "r"(line)
+            : "memory");
+    }
+    if (++f_slot == L::slots) f_slot = 0;
+    if (f_key) {
+      f_key = false;
+      return;
+    }
+    f_key = true;
+    --f_left;
+    if (++f_tile == f_nt && f_left > 0) {   // on to the next group or sequence
+      f_tile = 0;
+      if (++f_u == units) {
+        f_u = 0;
+        do {
+          f_nt = tiles_of(seq_len(a, ++f_b));
+        } while (f_nt == 0);
+      }
+      f_rows = rows_from(f_win = 0);
+    } else if (f_tile - f_win == 32) {
+      f_rows = rows_from(f_win = f_tile);
+    }
+  };
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < L::slots; ++i) feed();
+  int slot = 0;
+  uint32_t parity = 0;
+  // The next slot's copy has landed (false: it did not come in time).
+  volatile int never = 0;
+  auto landed = [&]() {
+    const bool ok = mbar_wait(bar + slot, parity, &never, kWaitNs);
+    return __all_sync(0xffffffffu, ok);
+  };
+  auto next_slot = [&]() {   // every lane has read the slot: it is filled again
+    __syncwarp();
+    feed();
+    if (++slot == L::slots) {
+      slot = 0;
+      parity ^= 1;
+    }
+  };
+  bool gave_up = false;
+  int count = 0;   // tiles done
+  for (int todo = piece; todo > 0;) {
+    const int t_end = todo < nt - tile ? tile + todo : nt;
     const int hk = u / a.gtiles, row0 = (u - hk * a.gtiles) * H;
     // queries of heads row0 + g (and + 8) of the group; rows beyond the group are zero
     uint32_t qf[L::steps][4];
@@ -261,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
       uint4 raw[D / 32];
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        // lane j's columns: 8 from 32 c + 8 j (bf16), 16 from 64 c' + 16 j (8-bit cache)
-        const int col = FP8 ? (c >> 1) * 64 + j * 16 + (c & 1) * 8 : c * 32 + j * 8;
+        // the columns of lane j's key chunks: 8 a chunk (bf16), 16 (8-bit cache)
+        const int col = FP8 ? L::k_chunk(c >> 1, j) * 16 + (c & 1) * 8 : L::k_chunk(c, j) * 8;
         raw[c] = on ? __ldg(reinterpret_cast<const uint4*>(qr + col)) : make_uint4(0u, 0u, 0u, 0u);
       }
       if (r < HT) qs[r] = a.scale * kLog2e;
@@ -300,8 +395,6 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
     }
     float o[HT][L::mt][4];
     float m[HT], l[HT];
-    bool careful = false;
-  again:
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
       m[h] = __int_as_float(0xff800000);
@@ -311,63 +404,40 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[h][i][e] = 0.f;
     }
-    // cache row of tile t's first token, for the 32 tiles from `win` on (lane i: tile win + i); 0xffffffff: no page
-    int win = tile;
-    auto rows_of = [&](int t) -> uint32_t {
-      uint32_t r = 0xFFFFFFFFu;
-      if (t < t_end) {
-        const int col = t / tpp;
-        const int pid = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + col);
-        if (pid >= 0 && pid < a.n_pages)
-          r = (static_cast<uint32_t>(pid) * a.Hkv + hk) * a.page_size + static_cast<uint32_t>(t - col * tpp) * 16u;
-        else if (u == 0 && (t == tile || t == col * tpp))
-          record_device_error(a.errors);
-      }
-      return r;
-    };
-    uint32_t rows = rows_of(win + lane);
-    auto row_at = [&](int t) { return __shfl_sync(0xffffffffu, rows, t - win); };
-    const unsigned char* kbase = static_cast<const unsigned char*>(a.k);
-    const unsigned char* vbase = static_cast<const unsigned char*>(a.v);
-    uint4 kr[2][L::kvecs];
-    uint32_t vr[4][L::vwords];
-    uint32_t row = row_at(tile);
-    bool have = row != 0xFFFFFFFFu;
-    load_k<D, FP8>(kbase + static_cast<size_t>(have ? row : 0u) * (D * L::esz), g, j, kr);
-    load_v<D, FP8>(vbase + static_cast<size_t>(have ? row : 0u) * (D * L::esz), g, j, vr);
+#pragma unroll 1
     for (int t = tile; t < t_end; ++t) {
-      const int left = have ? n - t * 16 : 0, live = left < 16 ? left : 16;   // tokens of this tile that count
+      if (!landed()) {
+        gave_up = true;
+        break;
+      }
+      const int left = (f_have >> (count & 31)) & 1u ? n - t * 16 : 0, live = left < 16 ? left : 16;   // tokens that count
+      ++count;
       float s[2][4];
+      {
+        const uint32_t base = ring + slot * L::slot;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < 2; ++r) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[r][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[r][e] = 0.f;
+          uint4 kr[L::kvecs];
 #pragma unroll
-        for (int c = 0; c < L::kvecs; ++c) {
-          const uint32_t w[4] = {kr[r][c].x, kr[r][c].y, kr[r][c].z, kr[r][c].w};
-          if (FP8) {
+          for (int c = 0; c < L::kvecs; ++c) kr[c] = lds128(base + L::place(g + 8 * r, L::k_chunk(c, j) * 16));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_f16(s[r], qf[4 * c + i], e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xFFFFu)),
-                      e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16)));
-          } else {
-            mma_bf16(s[r], qf[2 * c], w[0], w[1]);
-            mma_bf16(s[r], qf[2 * c + 1], w[2], w[3]);
+          for (int c = 0; c < L::kvecs; ++c) {
+            const uint32_t w[4] = {kr[c].x, kr[c].y, kr[c].z, kr[c].w};
+            if (FP8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_f16(s[r], qf[4 * c + i], e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xFFFFu)),
+                        e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16)));
+            } else {
+              mma_bf16(s[r], qf[2 * c], w[0], w[1]);
+              mma_bf16(s[r], qf[2 * c + 1], w[2], w[3]);
+            }
           }
         }
       }
-      // the next keys
-      bool next_have = false;
-      uint32_t next_row = 0;
-      if (t + 1 < t_end) {
-        if (t + 1 - win == 32) {
-          win = t + 1;
-          rows = rows_of(win + lane);
-        }
-        next_row = row_at(t + 1);
-        next_have = next_row != 0xFFFFFFFFu;
-        load_k<D, FP8>(kbase + static_cast<size_t>(next_have ? next_row : 0u) * (D * L::esz), g, j, kr);
-      }
+      next_slot();
       // softmax of the tile: lane (g, j) has heads g (and g + 8), tokens 8 r + 2 j and + 1
       uint32_t hi[HT][2], lo[HT][2];
 #pragma unroll
@@ -411,9 +481,38 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
             const __half2 t2 = *reinterpret_cast<const __half2*>(&hi[h][r]);
             lo[h][r] = pack_f16x2(p[2 * r] - __low2float(t2), p[2 * r + 1] - __high2float(t2));
           } else {
-            hi[h][r] = pack_bf16x2(p[2 * r], p[2 * r + 1]);
-            lo[h][r] = pack_bf16x2(p[2 * r] - __uint_as_float(hi[h][r] << 16),
-                                   p[2 * r + 1] - __uint_as_float(hi[h][r] & 0xFFFF0000u));
+            constexpr float kLeast = 1.17549435e-38f;   // 2^-126
+            const uint32_t x = __float_as_uint(p[2 * r]), y = __float_as_uint(p[2 * r + 1]);
+            hi[h][r] = __byte_perm(x, y, 0x7632);
+            lo[h][r] = round_bf16x2(
+                fmaxf(p[2 * r] - __uint_as_float(x & 0xFFFF0000u), fminf(p[2 * r], kLeast)),
+                fmaxf(p[2 * r + 1] - __uint_as_float(y & 0xFFFF0000u), fminf(p[2 * r + 1], kLeast)));
+          }
+        }
+      }
+      if (!landed()) {
+        gave_up = true;
+        break;
+      }
+      uint32_t vr[4][L::vwords];
+      {
+        const uint32_t base = ring + slot * L::slot;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int tok = 2 * j + (r & 1) + 8 * (r >> 1);
+          if (L::vwords == 2) {
+            const uint2 w = lds64(base + L::place(tok, g * 8));
+            vr[r][0] = w.x;
+            vr[r][1] = w.y;
+          } else {
+#pragma unroll
+            for (int c = 0; c < L::vwords / 4; ++c) {
+              const uint4 w = lds128(base + L::place(tok, c * 128 + g * 16));
+              vr[r][4 * c] = w.x;
+              vr[r][4 * c + 1] = w.y;
+              vr[r][4 * c + 2] = w.z;
+              vr[r][4 * c + 3] = w.w;
+            }
           }
         }
       }
@@ -443,39 +542,22 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
             }
           }
         } else {
-          uint32_t va[4] = {__byte_perm(vr[0][w], vr[1][w], 0x5410), __byte_perm(vr[0][w], vr[1][w], 0x7632),
+          const uint32_t va[4] = {__byte_perm(vr[0][w], vr[1][w], 0x5410), __byte_perm(vr[0][w], vr[1][w], 0x7632),
                                   __byte_perm(vr[2][w], vr[3][w], 0x5410), __byte_perm(vr[2][w], vr[3][w], 0x7632)};
 #pragma unroll
-          for (int h = 0; h < HT; ++h) mma_bf16(o[h][w], va, hi[h][0], hi[h][1]);
-          if (careful) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) va[i] = finite_bf16x2(va[i]);
+          for (int h = 0; h < HT; ++h) {
+            mma_bf16(o[h][w], va, hi[h][0], hi[h][1]);
+            mma_bf16(o[h][w], va, lo[h][0], lo[h][1]);
           }
-#pragma unroll
-          for (int h = 0; h < HT; ++h) mma_bf16(o[h][w], va, lo[h][0], lo[h][1]);
         }
       }
-      if (t + 1 < t_end)
-        load_v<D, FP8>(vbase + static_cast<size_t>(next_have ? next_row : 0u) * (D * L::esz), g, j, vr);
-      have = next_have;
+      next_slot();
     }
-    if (!FP8 && !careful) {
-      bool nan = false;
-#pragma unroll
-      for (int h = 0; h < HT; ++h)
-#pragma unroll
-        for (int i = 0; i < L::mt; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) nan |= o[h][i][e] != o[h][i][e];
-      if (__any_sync(0xffffffffu, nan)) {
-        careful = true;
-        goto again;
-      }
-    }
+    if (gave_up) break;
     // lane (g, j): o[h][..] has heads 8 h + 2 j (elements 0, 2) and + 1 (1, 3), columns v_col and + 1
     const bool whole = tile == 0 && t_end == nt;
-    const int slot = x == x0 ? 0 : 1;
-    float* part = a.parts + (static_cast<size_t>(gw) * 2 + slot) * part_floats<D, HT>();
+    const int part_slot = todo == piece ? 0 : 1;
+    float* part = a.parts + (static_cast<size_t>(gw) * 2 + part_slot) * part_floats<D, HT>();
     const float vs = FP8 ? __ldg(a.v_scale + hk) / kPScale : 1.f;
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
@@ -506,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
       }
     }
     // on to the next group or sequence
-    x += t_end - tile;
-    if (x < x1) {
+    todo -= t_end - tile;
+    if (todo > 0) {
       tile = 0;
       if (++u == units) {
         u = 0;
@@ -518,26 +600,38 @@ __global__ void __launch_bounds__(kThreads, HT == 1 ? 3 : 2) attn_kernel(AttnArg
       }
     }
   }
+  if (gave_up) {   // count it, and let the copies that may still come land before the memory is another's
+    if (lane == 0) atomicAdd(a.timeouts, 1u);
+    for (int i = 0; i < L::slots; ++i) {
+      mbar_wait(bar + slot, parity, &never, kWaitNs / 16);
+      if (++slot == L::slots) {
+        slot = 0;
+        parity ^= 1;
+      }
+    }
+  }
 }
 
 // Joins the parts of the groups that were cut, one block per (sequence, query head), and writes the rows of empty
 // sequences.
 template <int D, int HT, typename TO>
-__global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a) {
-  constexpr int H = 8 * HT, kCols = D / 32;
-  __shared__ long long scan[kWarps];
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
+  constexpr int H = 8 * HT, kJoinWarps = kJoinThreads / 32, kLanes = D / 4, kRows = kJoinThreads / kLanes;
+  extern __shared__ float weight[];   // exp2(m - max m) of each part
+  __shared__ long long scan[kJoinWarps];
   __shared__ long long start_of_b;
-  __shared__ float red[kWarps][D + 2];
+  __shared__ float red_m[kJoinWarps], red_l[kJoinWarps];
+  __shared__ float4 red[kRows][kLanes];
   const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
   const int hk = hq / a.G, in_group = hq - hk * a.G, gt = in_group / H, head = in_group - gt * H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int units = a.Hkv * a.gtiles;
-  const int per = (a.B + kThreads - 1) / kThreads, b_lo = threadIdx.x * per;
+  const int per = (a.B + kJoinThreads - 1) / kJoinThreads, b_lo = threadIdx.x * per;
   const int b_hi = b_lo + per < a.B ? b_lo + per : a.B;
   long long mine = 0;
   for (int i = b_lo; i < b_hi; ++i) mine += static_cast<long long>(tiles_of(seq_len(a, i))) * units;
   long long total;
-  const long long pre = block_prefix(mine, scan, total);
+  const long long pre = block_prefix<kJoinWarps>(mine, scan, total);
   if (b >= b_lo && b < b_hi) {
     long long p = pre;
     for (int i = b_lo; i < b; ++i) p += static_cast<long long>(tiles_of(seq_len(a, i))) * units;
@@ -546,73 +640,95 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a) {
   __syncthreads();
   const int nt = tiles_of(seq_len(a, b));
   TO* out = static_cast<TO*>(a.out) + (static_cast<size_t>(b) * a.Hq + hq) * D;
-  // every thread of the first kernel's grid is done, and its writes are visible, behind this line
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (nt == 0) {
-    for (int c = threadIdx.x * 2; c < D; c += kThreads * 2) store2(out + c, 0.f, 0.f);
+  if (nt == 0) {   // the first kernel does not touch these rows, and it began behind what came before both
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int c = threadIdx.x * 2; c < D; c += kJoinThreads * 2) store2(out + c, 0.f, 0.f);
     if (a.lse && threadIdx.x == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = __int_as_float(0xff800000);
     return;
   }
   const long long p0 = start_of_b + static_cast<long long>(hk * a.gtiles + gt) * nt, p1 = p0 + nt;
   const Pieces pieces(total, a.warps);
-  const int w0 = pieces.owner(p0), w1 = pieces.owner(p1 - 1);
-  if (w0 == w1) return;   // written whole
+  const int w0 = pieces.owner(p0), parts = pieces.owner(p1 - 1) - w0 + 1;
+  if (parts == 1) return;   // written whole
+  const float* base = a.parts + static_cast<size_t>(w0) * 2 * part_floats<D, HT>();
   const int first_slot = pieces.start(w0) == p0 ? 0 : 1;
-  auto part_of = [&](int w) -> const float* {
-    return a.parts + (static_cast<size_t>(w) * 2 + (w == w0 ? first_slot : 0)) * part_floats<D, HT>();
-  };
+  auto part_of = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? first_slot : 0)) * part_floats<D, HT>(); };
+  // every thread of the first kernel's grid is done, and its writes are visible, behind this line
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float m = __int_as_float(0xff800000);
-  for (int w = w0 + static_cast<int>(threadIdx.x); w <= w1; w += kThreads) m = fmaxf(m, __ldcg(part_of(w) + head));
+  for (int i = threadIdx.x; i < parts; i += kJoinThreads) m = fmaxf(m, weight[i] = __ldcg(part_of(i) + head));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[warp][0] = m;
+  if (lane == 0) red_m[warp] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red[w][0]);
-  __syncthreads();
-  const float base = m == __int_as_float(0xff800000) ? 0.f : m;
-  float l = 0.f, acc[kCols];
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-#pragma unroll 8
-  for (int w = w0 + warp; w <= w1; w += kWarps) {
-    const float* p = part_of(w);
-    const float k = exp2f(__ldcg(p + head) - base);
-    l = fmaf(__ldcg(p + H + head), k, l);
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] = fmaf(__ldcg(p + 2 * H + head * D + c * 32 + lane), k, acc[c]);
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red_m[w]);
+  const float top = m == __int_as_float(0xff800000) ? 0.f : m;
+  float l = 0.f;
+  for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+    const float k = exp2f(weight[i] - top);
+    weight[i] = k;
+    l = fmaf(__ldcg(part_of(i) + H + head), k, l);
   }
-  if (lane == 0) red[warp][D] = l;
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) red[warp][c * 32 + lane] = acc[c];
+  l = warp_sum(l);
+  if (lane == 0) red_l[warp] = l;
+  __syncthreads();
+  const int col = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = first; i < parts; i += kRows) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(i) + 2 * H + head * D) + col);
+    const float k = weight[i];
+    acc.x = fmaf(v.x, k, acc.x);
+    acc.y = fmaf(v.y, k, acc.y);
+    acc.z = fmaf(v.z, k, acc.z);
+    acc.w = fmaf(v.w, k, acc.w);
+  }
+  red[first][col] = acc;
   __syncthreads();
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) l += red[w][D];
-  const float f = l == 0.f ? 0.f : gate_of(a, b, hq) / l;
-  for (int c = threadIdx.x * 2; c < D; c += kThreads * 2) {
-    float x = 0.f, y = 0.f;
+  for (int w = 0; w < kJoinWarps; ++w) l += red_l[w];
+  if (threadIdx.x < kLanes) {
+    const float f = l == 0.f ? 0.f : gate_of(a, b, hq) / l;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      x += red[w][c];
-      y += red[w][c + 1];
+    for (int r = 1; r < kRows; ++r) {
+      const float4 v = red[r][col];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
     }
-    store2(out + c, x * f, y * f);
+    store2(out + 4 * col, acc.x * f, acc.y * f);
+    store2(out + 4 * col + 2, acc.z * f, acc.w * f);
   }
   if (a.lse && threadIdx.x == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = (m + log2f(l)) * kLn2;
 }
 
 template <int D, bool FP8, int HT, typename TO>
 zmoe_status launch(AttnArgs a, cudaStream_t s) {
-  const int blocks = num_sms() * (HT == 1 ? 3 : 2);
+  using L = Lay<D, FP8, HT>;
+  static_assert(L::blocks * kWarps <= kMaxWarpsPerSm, "the workspace holds the warps' parts");
+  const int blocks = num_sms() * L::blocks;
   a.warps = blocks * kWarps;
-  static_assert((HT == 1 ? 3 : 2) * kWarps <= kMaxWarpsPerSm, "the workspace holds the warps' parts");
-  attn_kernel<D, FP8, HT, TO><<<blocks, kThreads, 0, s>>>(a);
+  // the cache as lines of 128 bytes at least (two rows of an 8-bit cache of 64 columns), a box a tile or half of one
+  const cuuint64_t rows = static_cast<cuuint64_t>(a.n_pages) * a.Hkv * a.page_size;
+  const cuuint64_t dims[2] = {L::row < 128 ? 128 : L::row, rows * L::row / (L::row < 128 ? 128 : L::row)};
+  const cuuint64_t stride[1] = {dims[0]};
+  const cuuint32_t box[2] = {128, L::row < 128 ? 8 : 16};
+  CUtensorMap km, vm;
+  if (!encode_map(&km, a.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dims, stride, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(&vm, a.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dims, stride, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return fail(ZMOE_ERR_CUDA, "zmoe_paged_attention: the cache's tensor map cannot be made");
+  if (cudaFuncSetAttribute(attn_kernel<D, FP8, HT, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem) != cudaSuccess)
+    return check_launch("zmoe_paged_attention: shared memory attribute");
+  attn_kernel<D, FP8, HT, TO><<<blocks, kThreads, L::smem, s>>>(km, vm, a);
   zmoe_status st = check_launch("zmoe_paged_attention");
   if (st != ZMOE_OK) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.Hq);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.warps) * 4;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -672,8 +788,8 @@ zmoe_status zmoe_paged_attention(const void* q, const void* k_cache, const void*
                "zmoe_paged_attention: q, the caches and out must be 16-byte aligned");
   ZMOE_REQUIRE(static_cast<long long>(max_pages) * page_size <= 0x7fffffffLL,
                "zmoe_paged_attention: max_pages * page_size overflows int32");
-  ZMOE_REQUIRE(static_cast<unsigned long long>(n_pages) * Hkv * page_size < 0xffffffffULL,
-               "zmoe_paged_attention: n_pages * Hkv * page_size overflows 32 bits");
+  ZMOE_REQUIRE(static_cast<unsigned long long>(n_pages) * Hkv * page_size < 0x7fffffffULL,
+               "zmoe_paged_attention: n_pages * Hkv * page_size overflows int32");
   ZMOE_REQUIRE(static_cast<long long>(B) * Hq <= 0x7fffffffLL, "zmoe_paged_attention: B * Hq overflows int32");
   if (!workspace || ws_bytes < zmoe_paged_attention_workspace_size(B, Hq, Hkv, D))
     return fail(ZMOE_ERR_WORKSPACE_TOO_SMALL,
@@ -688,6 +804,7 @@ zmoe_status zmoe_paged_attention(const void* q, const void* k_cache, const void*
   a.max_pages = max_pages; a.n_pages = n_pages; a.page_size = page_size;
   a.out = out; a.lse = lse; a.parts = static_cast<float*>(workspace);
   a.errors = device_error_counter();
+  a.timeouts = device_timeout_counter();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = out_dtype == ZMOE_BF16;
   if (kv_dtype == ZMOE_E4M3) return D == 64 ? launch_out<64, true>(a, bf, s) : launch_out<128, true>(a, bf, s);
