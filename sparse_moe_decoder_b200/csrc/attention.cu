@@ -149,22 +149,30 @@ struct Lay {
   static constexpr int vwords = row / 32;          // 32-bit words of a value row per lane (8 lanes a row)
   static constexpr int steps = D / 16;             // 16-column steps of the first product
   static constexpr int mt = D / 16;                // 16-column tiles of the output
-  static constexpr int slot = 16 * row;            // bytes of a tile's keys or values
-  static constexpr int blocks = HT == 1 ? 4 : 2;   // CTAs an SM: 128 or 255 registers a thread
-  static constexpr int ring = HT == 1 ? 12288 : 24576;   // bytes a warp
-  static constexpr int slots = ring / slot < 12 ? ring / slot : 12;
+  static constexpr int half = 16 * row;            // bytes of a tile's keys or values
+  static constexpr int tiles = 4096 / half;        // tiles of a step
+  static constexpr int slot = 8192;                // bytes of a step: its keys, its values
+  static constexpr int blocks = HT == 1 ? 3 : 2;   // CTAs an SM: 168 or 255 registers a thread
+  static constexpr int slots = HT == 1 ? 2 : 3;
   static constexpr int smem = kWarps * slots * slot + 1024;   // the ring starts on 1024 bytes
-  static_assert(slots >= 2 && slot % 1024 == 0, "whole swizzle atoms");
+  static_assert(half % 1024 == 0 && tiles >= 1, "whole swizzle atoms");
 
   // Chunk c of lane j's share of a key row, in 16-byte chunks of the row.
   __device__ __forceinline__ static int k_chunk(int c, int j) { return row >= 128 ? (c >> 1) * 8 + 2 * j + (c & 1) : j; }
-  // Byte `at` of token r's row within the slot.
+  // Byte `at` of token r's row within a tile.
   __device__ __forceinline__ static uint32_t place(int r, int at) {
     const uint32_t x = row == 256 ? static_cast<uint32_t>((at >> 7) * 2048 + r * 128 + (at & 127))
                                   : static_cast<uint32_t>(r * row + at);
     return x ^ (((x >> 7) & 7u) << 4);
   }
 };
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
 
 __device__ __forceinline__ uint4 lds128(uint32_t p) {
   uint4 r;
@@ -217,6 +225,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
   uint64_t* bar = bars[warp];
   const uint32_t ring = ((smem_u32(ring_raw) + 1023u) & ~1023u) + static_cast<uint32_t>(warp * L::slots * L::slot);
   if (lane == 0) {
+    asm volatile("prefetch.tensormap [%0];\n\tprefetch.tensormap [%1];" ::"l"(reinterpret_cast<uint64_t>(&kmap)),
+                 "l"(reinterpret_cast<uint64_t>(&vmap)));
     for (int i = 0; i < L::slots; ++i) mbar_init(bar + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -255,60 +265,51 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
   int b = at_b[warp], n = seq_len(a, b), nt = tiles_of(n);
   int u = static_cast<int>(divide(at_off[warp], nt)), tile = static_cast<int>(at_off[warp] - static_cast<long long>(u) * nt);
 
-  // The feeder runs ahead of the products: keys and values of one tile after another, each into the next slot.
+  // The feeder runs ahead of the products: the keys and values of a step's tiles into the next slot.
   const int tpp = a.page_size >> 4;   // tiles per page
   int f_b = b, f_u = u, f_tile = tile, f_nt = nt, f_win = tile, f_slot = 0;
   int f_left = piece;                 // tiles to feed
-  bool f_key = true;
-  uint32_t f_row = 0, f_have = 0;     // the tile's cache row; bit t & 31: the t-th tile of the piece has a page
-  int f_count = 0;
-  // cache rows of the 32 tiles from f_win on (lane i: tile f_win + i); 0xffffffff: no page
-  auto rows_from = [&](int win) -> uint32_t {
+  uint32_t f_have = 0;                // which tiles of the steps in the ring have a page: the oldest step lowest
+  // cache lines of the 32 tiles from f_win on (lane i: tile f_win + i); -1: no page
+  auto lines_from = [&](int win) -> int {
     const int t = win + lane;
-    uint32_t r = 0xFFFFFFFFu;
+    int line = -1;
     if (t < f_nt && t - f_tile < f_left) {
       const int col = t / tpp;
       const int pid = __ldg(a.table + static_cast<size_t>(f_b) * a.max_pages + col);
       if (pid >= 0 && pid < a.n_pages)
-        r = (static_cast<uint32_t>(pid) * a.Hkv + f_u / a.gtiles) * a.page_size + static_cast<uint32_t>(t - col * tpp) * 16u;
+        line = ((pid * a.Hkv + f_u / a.gtiles) * a.page_size + (t - col * tpp) * 16) >> (L::row == 64 ? 1 : 0);
       else if (f_u == 0 && (t == f_tile || t == col * tpp))
         record_device_error(a.errors);
     }
-    return r;
+    return line;
   };
-  uint32_t f_rows = rows_from(f_win);
-  auto feed = [&]() {
+  int f_lines = lines_from(f_win);
+  auto feed = [&](int ahead) {   // ahead: steps in the ring before this one
     if (f_left == 0) return;
-    if (f_key) {
-      const uint32_t r = __shfl_sync(0xffffffffu, f_rows, f_tile - f_win);
-      const bool have = r != 0xFFFFFFFFu;
-      f_row = have ? r : 0u;   // any row in its place: its tokens do not count
-      const uint32_t bit = 1u << (f_count & 31);
-      f_have = have ? f_have | bit : f_have & ~bit;
-      ++f_count;
-    }
-    if (lane == 0) {
-      uint64_t* full = bar + f_slot;
-      const CUtensorMap* map = f_key ? &kmap : &vmap;
-      const uint32_t dst = ring + f_slot * L::slot;
-      mbar_expect_tx(full, L::slot);
-      const int line = static_cast<int>(L::row == 64 ? f_row >> 1 : f_row);
+    const int rest = f_nt - f_tile < f_left ? f_nt - f_tile : f_left, here = rest < L::tiles ? rest : L::tiles;
+    uint64_t* full = bar + f_slot;
+    const uint32_t dst = ring + f_slot * L::slot;
+    if (lane == 0) mbar_expect_tx(full, here * 2 * L::half);
+    uint32_t have = 0;
 #pragma unroll
-      for (int half = 0; half < (L::row == 256 ? 2 : 1); ++half)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-                dst + half * 2048),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(full)), "r"(half * 128), "r"(line)
-            : "memory");
+    for (int i = 0; i < L::tiles; ++i) {
+      const int line = __shfl_sync(0xffffffffu, f_lines, f_tile - f_win + i);
+      if (line >= 0) have |= 1u << i;
+      if (lane == 0 && i < here) {
+        const int at = line >= 0 ? line : 0;   // any rows in place of none: these tokens do not count
+#pragma unroll
+        for (int c = 0; c < (L::row == 256 ? 2 : 1); ++c) {
+          tma_2d(dst + i * L::half + c * 2048, &kmap, full, c * 128, at);
+          tma_2d(dst + 4096 + i * L::half + c * 2048, &vmap, full, c * 128, at);
+        }
+      }
     }
+    f_have |= have << (ahead * L::tiles);
     if (++f_slot == L::slots) f_slot = 0;
-    if (f_key) {
-      f_key = false;
-      return;
-    }
-    f_key = true;
-    --f_left;
-    if (++f_tile == f_nt && f_left > 0) {   // on to the next group or sequence
+    f_left -= here;
+    f_tile += here;
+    if (f_tile == f_nt && f_left > 0) {   // on to the next group or sequence
       f_tile = 0;
       if (++f_u == units) {
         f_u = 0;
@@ -316,14 +317,14 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
           f_nt = tiles_of(seq_len(a, ++f_b));
         } while (f_nt == 0);
       }
-      f_rows = rows_from(f_win = 0);
+      f_lines = lines_from(f_win = 0);
     } else if (f_tile - f_win == 32) {
-      f_rows = rows_from(f_win = f_tile);
+      f_lines = lines_from(f_win = f_tile);
     }
   };
   __syncwarp();
 #pragma unroll 1
-  for (int i = 0; i < L::slots; ++i) feed();
+  for (int i = 0; i < L::slots; ++i) feed(i);
   int slot = 0;
   uint32_t parity = 0;
   // The next slot's copy has landed (false: it did not come in time).
@@ -332,16 +333,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
     const bool ok = mbar_wait(bar + slot, parity, &never, kWaitNs);
     return __all_sync(0xffffffffu, ok);
   };
-  auto next_slot = [&]() {   // every lane has read the slot: it is filled again
-    __syncwarp();
-    feed();
-    if (++slot == L::slots) {
-      slot = 0;
-      parity ^= 1;
-    }
-  };
   bool gave_up = false;
-  int count = 0;   // tiles done
   for (int todo = piece; todo > 0;) {
     const int t_end = todo < nt - tile ? tile + todo : nt;
     const int hk = u / a.gtiles, row0 = (u - hk * a.gtiles) * H;
@@ -405,52 +397,59 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
         for (int e = 0; e < 4; ++e) o[h][i][e] = 0.f;
     }
 #pragma unroll 1
-    for (int t = tile; t < t_end; ++t) {
+    for (int t = tile; t < t_end; t += L::tiles) {
       if (!landed()) {
         gave_up = true;
         break;
       }
-      const int left = (f_have >> (count & 31)) & 1u ? n - t * 16 : 0, live = left < 16 ? left : 16;   // tokens that count
-      ++count;
-      float s[2][4];
-      {
-        const uint32_t base = ring + slot * L::slot;
+      const uint32_t base = ring + slot * L::slot;
+      // tokens of each tile that count
+      int live[L::tiles];
+#pragma unroll
+      for (int i = 0; i < L::tiles; ++i) {
+        const int left = t + i < t_end && ((f_have >> i) & 1u) ? n - (t + i) * 16 : 0;
+        live[i] = left < 16 ? left : 16;
+      }
+      float s[L::tiles][2][4];
+#pragma unroll
+      for (int i = 0; i < L::tiles; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+          float(&d)[4] = s[i][r];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[r][e] = 0.f;
+          for (int e = 0; e < 4; ++e) d[e] = 0.f;
           uint4 kr[L::kvecs];
 #pragma unroll
-          for (int c = 0; c < L::kvecs; ++c) kr[c] = lds128(base + L::place(g + 8 * r, L::k_chunk(c, j) * 16));
+          for (int c = 0; c < L::kvecs; ++c)
+            kr[c] = lds128(base + i * L::half + L::place(g + 8 * r, L::k_chunk(c, j) * 16));
 #pragma unroll
           for (int c = 0; c < L::kvecs; ++c) {
             const uint32_t w[4] = {kr[c].x, kr[c].y, kr[c].z, kr[c].w};
             if (FP8) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_f16(s[r], qf[4 * c + i], e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xFFFFu)),
-                        e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16)));
+              for (int q = 0; q < 4; ++q)
+                mma_f16(d, qf[4 * c + q], e4m3x2_to_f16x2(static_cast<uint16_t>(w[q] & 0xFFFFu)),
+                        e4m3x2_to_f16x2(static_cast<uint16_t>(w[q] >> 16)));
             } else {
-              mma_bf16(s[r], qf[2 * c], w[0], w[1]);
-              mma_bf16(s[r], qf[2 * c + 1], w[2], w[3]);
+              mma_bf16(d, qf[2 * c], w[0], w[1]);
+              mma_bf16(d, qf[2 * c + 1], w[2], w[3]);
             }
           }
         }
-      }
-      next_slot();
-      // softmax of the tile: lane (g, j) has heads g (and g + 8), tokens 8 r + 2 j and + 1
-      uint32_t hi[HT][2], lo[HT][2];
+      // softmax of the step: lane (g, j) has heads g (and g + 8), of each tile the tokens 8 r + 2 j and + 1
+      uint32_t hi[L::tiles][HT][2], lo[L::tiles][HT][2];
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
-        float z[4];
+        float z[L::tiles][4];
         float top = m[h];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = 8 * (i >> 1) + 2 * j + (i & 1);
-          z[i] = s[i >> 1][2 * h + (i & 1)] * qs[h];
-          if (tok >= live) z[i] = __int_as_float(0xff800000);
-          top = fmaxf(top, z[i]);
-        }
+        for (int i = 0; i < L::tiles; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            z[i][e] = s[i][e >> 1][2 * h + (e & 1)] * qs[h];
+            if (8 * (e >> 1) + 2 * j + (e & 1) >= live[i]) z[i][e] = __int_as_float(0xff800000);
+            top = fmaxf(top, z[i][e]);
+          }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         if (__any_sync(0xffffffffu, top > m[h])) {
@@ -466,48 +465,48 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
           }
           m[h] = top;
         }
-        const float base = m[h] == __int_as_float(0xff800000) ? 0.f : m[h];
-        float p[4];
+        const float zero = m[h] == __int_as_float(0xff800000) ? 0.f : m[h];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[i] = exp2f(z[i] - base);
-          l[h] += p[i];
-          p[i] *= kPScale;
-        }
+        for (int i = 0; i < L::tiles; ++i) {
+          float p[4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (FP8) {
-            hi[h][r] = pack_f16x2(p[2 * r], p[2 * r + 1]);
-            const __half2 t2 = *reinterpret_cast<const __half2*>(&hi[h][r]);
-            lo[h][r] = pack_f16x2(p[2 * r] - __low2float(t2), p[2 * r + 1] - __high2float(t2));
-          } else {
-            constexpr float kLeast = 1.17549435e-38f;   // 2^-126
-            const uint32_t x = __float_as_uint(p[2 * r]), y = __float_as_uint(p[2 * r + 1]);
-            hi[h][r] = __byte_perm(x, y, 0x7632);
-            lo[h][r] = round_bf16x2(
-                fmaxf(p[2 * r] - __uint_as_float(x & 0xFFFF0000u), fminf(p[2 * r], kLeast)),
-                fmaxf(p[2 * r + 1] - __uint_as_float(y & 0xFFFF0000u), fminf(p[2 * r + 1], kLeast)));
+          for (int e = 0; e < 4; ++e) {
+            p[e] = exp2f(z[i][e] - zero);
+            l[h] += p[e];
+            p[e] *= kPScale;
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (FP8) {
+              hi[i][h][r] = pack_f16x2(p[2 * r], p[2 * r + 1]);
+              const __half2 t2 = *reinterpret_cast<const __half2*>(&hi[i][h][r]);
+              lo[i][h][r] = pack_f16x2(p[2 * r] - __low2float(t2), p[2 * r + 1] - __high2float(t2));
+            } else {
+              constexpr float kLeast = 1.17549435e-38f;   // 2^-126
+              const uint32_t x = __float_as_uint(p[2 * r]), y = __float_as_uint(p[2 * r + 1]);
+              hi[i][h][r] = __byte_perm(x, y, 0x7632);
+              lo[i][h][r] = round_bf16x2(
+                  fmaxf(p[2 * r] - __uint_as_float(x & 0xFFFF0000u), fminf(p[2 * r], kLeast)),
+                  fmaxf(p[2 * r + 1] - __uint_as_float(y & 0xFFFF0000u), fminf(p[2 * r + 1], kLeast)));
+            }
           }
         }
       }
-      if (!landed()) {
-        gave_up = true;
-        break;
-      }
-      uint32_t vr[4][L::vwords];
-      {
-        const uint32_t base = ring + slot * L::slot;
+#pragma unroll
+      for (int i = 0; i < L::tiles; ++i) {
+        uint32_t vr[4][L::vwords];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int tok = 2 * j + (r & 1) + 8 * (r >> 1);
+          const uint32_t from = base + 4096 + i * L::half;
           if (L::vwords == 2) {
-            const uint2 w = lds64(base + L::place(tok, g * 8));
+            const uint2 w = lds64(from + L::place(tok, g * 8));
             vr[r][0] = w.x;
             vr[r][1] = w.y;
           } else {
 #pragma unroll
             for (int c = 0; c < L::vwords / 4; ++c) {
-              const uint4 w = lds128(base + L::place(tok, c * 128 + g * 16));
+              const uint4 w = lds128(from + L::place(tok, c * 128 + g * 16));
               vr[r][4 * c] = w.x;
               vr[r][4 * c + 1] = w.y;
               vr[r][4 * c + 2] = w.z;
@@ -515,43 +514,50 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
             }
           }
         }
-      }
-      if (live < 16) {   // what lies behind the sequence's end may be anything, and 0 x NaN is NaN
+        if (live[i] < 16) {   // what lies behind the sequence's end may be anything, and 0 x NaN is NaN
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (2 * j + (r & 1) + 8 * (r >> 1) >= live) {
+          for (int r = 0; r < 4; ++r)
+            if (2 * j + (r & 1) + 8 * (r >> 1) >= live[i]) {
 #pragma unroll
-            for (int w = 0; w < L::vwords; ++w) vr[r][w] = 0u;
-          }
-      }
+              for (int w = 0; w < L::vwords; ++w) vr[r][w] = 0u;
+            }
+        }
 #pragma unroll
-      for (int w = 0; w < L::vwords; ++w) {
-        if (FP8) {
+        for (int w = 0; w < L::vwords; ++w) {
+          if (FP8) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {   // columns 4 w + 2 half, + 1 of the lane's share
-            const uint32_t x = __byte_perm(vr[0][w], vr[1][w], half ? 0x7362 : 0x5140);
-            const uint32_t y = __byte_perm(vr[2][w], vr[3][w], half ? 0x7362 : 0x5140);
-            const uint32_t va[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(x & 0xFFFFu)),
-                                    e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16)),
-                                    e4m3x2_to_f16x2(static_cast<uint16_t>(y & 0xFFFFu)),
-                                    e4m3x2_to_f16x2(static_cast<uint16_t>(y >> 16))};
+            for (int half = 0; half < 2; ++half) {   // columns 4 w + 2 half, + 1 of the lane's share
+              const uint32_t x = __byte_perm(vr[0][w], vr[1][w], half ? 0x7362 : 0x5140);
+              const uint32_t y = __byte_perm(vr[2][w], vr[3][w], half ? 0x7362 : 0x5140);
+              const uint32_t va[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(x & 0xFFFFu)),
+                                      e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16)),
+                                      e4m3x2_to_f16x2(static_cast<uint16_t>(y & 0xFFFFu)),
+                                      e4m3x2_to_f16x2(static_cast<uint16_t>(y >> 16))};
+#pragma unroll
+              for (int h = 0; h < HT; ++h) {
+                mma_f16(o[h][2 * w + half], va, hi[i][h][0], hi[i][h][1]);
+                mma_f16(o[h][2 * w + half], va, lo[i][h][0], lo[i][h][1]);
+              }
+            }
+          } else {
+            const uint32_t va[4] = {__byte_perm(vr[0][w], vr[1][w], 0x5410), __byte_perm(vr[0][w], vr[1][w], 0x7632),
+                                    __byte_perm(vr[2][w], vr[3][w], 0x5410), __byte_perm(vr[2][w], vr[3][w], 0x7632)};
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
-              mma_f16(o[h][2 * w + half], va, hi[h][0], hi[h][1]);
-              mma_f16(o[h][2 * w + half], va, lo[h][0], lo[h][1]);
+              mma_bf16(o[h][w], va, hi[i][h][0], hi[i][h][1]);
+              mma_bf16(o[h][w], va, lo[i][h][0], lo[i][h][1]);
             }
-          }
-        } else {
-          const uint32_t va[4] = {__byte_perm(vr[0][w], vr[1][w], 0x5410), __byte_perm(vr[0][w], vr[1][w], 0x7632),
-                                  __byte_perm(vr[2][w], vr[3][w], 0x5410), __byte_perm(vr[2][w], vr[3][w], 0x7632)};
-#pragma unroll
-          for (int h = 0; h < HT; ++h) {
-            mma_bf16(o[h][w], va, hi[h][0], hi[h][1]);
-            mma_bf16(o[h][w], va, lo[h][0], lo[h][1]);
           }
         }
       }
-      next_slot();
+      // every lane has read the slot: it is filled again
+      __syncwarp();
+      f_have >>= L::tiles;
+      feed(L::slots - 1);
+      if (++slot == L::slots) {
+        slot = 0;
+        parity ^= 1;
+      }
     }
     if (gave_up) break;
     // lane (g, j): o[h][..] has heads 8 h + 2 j (elements 0, 2) and + 1 (1, 3), columns v_col and + 1
@@ -617,10 +623,9 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
 template <int D, int HT, typename TO>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
   constexpr int H = 8 * HT, kJoinWarps = kJoinThreads / 32, kLanes = D / 4, kRows = kJoinThreads / kLanes;
-  extern __shared__ float weight[];   // exp2(m - max m) of each part
   __shared__ long long scan[kJoinWarps];
   __shared__ long long start_of_b;
-  __shared__ float red_m[kJoinWarps], red_l[kJoinWarps];
+  __shared__ float red_m[kRows], red_l[kRows];
   __shared__ float4 red[kRows][kLanes];
   const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
   const int hk = hq / a.G, in_group = hq - hk * a.G, gt = in_group / H, head = in_group - gt * H;
@@ -655,54 +660,73 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
   auto part_of = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? first_slot : 0)) * part_floats<D, HT>(); };
   // every thread of the first kernel's grid is done, and its writes are visible, behind this line
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float m = __int_as_float(0xff800000);
-  for (int i = threadIdx.x; i < parts; i += kJoinThreads) m = fmaxf(m, weight[i] = __ldcg(part_of(i) + head));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red_m[warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red_m[w]);
-  const float top = m == __int_as_float(0xff800000) ? 0.f : m;
-  float l = 0.f;
-  for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
-    const float k = exp2f(weight[i] - top);
-    weight[i] = k;
-    l = fmaf(__ldcg(part_of(i) + H + head), k, l);
-  }
-  l = warp_sum(l);
-  if (lane == 0) red_l[warp] = l;
-  __syncthreads();
+  // D / 4 lanes take every kRows-th part, 8 of them in flight, with a running maximum
+  constexpr int kBatch = 8;
   const int col = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
+  float m = __int_as_float(0xff800000), l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = first; i < parts; i += kRows) {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(i) + 2 * H + head * D) + col);
-    const float k = weight[i];
+  for (int i0 = first; i0 < parts; i0 += kRows * kBatch) {
+    float mi[kBatch], li[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int i = i0 + q * kRows;
+      mi[q] = __int_as_float(0xff800000);
+      if (i < parts) {
+        const float* p = part_of(i);
+        mi[q] = __ldcg(p + head);
+        li[q] = __ldcg(p + H + head);
+        v[q] = __ldcg(reinterpret_cast<const float4*>(p + 2 * H + head * D) + col);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) top = fmaxf(top, mi[q]);
+    const float zero = top == __int_as_float(0xff800000) ? 0.f : top;
+    const float keep = exp2f(m - zero);
+    l *= keep;
+    acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
+    m = top;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      if (i0 + q * kRows < parts) {
+        const float k = exp2f(mi[q] - zero);
+        l = fmaf(li[q], k, l);
+        acc.x = fmaf(v[q].x, k, acc.x);
+        acc.y = fmaf(v[q].y, k, acc.y);
+        acc.z = fmaf(v[q].z, k, acc.z);
+        acc.w = fmaf(v[q].w, k, acc.w);
+      }
+    }
+  }
+  red[first][col] = acc;
+  if (col == 0) {
+    red_m[first] = m;
+    red_l[first] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x >= kLanes) return;
+  float top = red_m[0];
+#pragma unroll
+  for (int r = 1; r < kRows; ++r) top = fmaxf(top, red_m[r]);
+  const float zero = top == __int_as_float(0xff800000) ? 0.f : top;
+  l = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (r >= parts) break;   // that row has no part
+    const float k = exp2f(red_m[r] - zero);
+    const float4 v = red[r][col];
+    l = fmaf(red_l[r], k, l);
     acc.x = fmaf(v.x, k, acc.x);
     acc.y = fmaf(v.y, k, acc.y);
     acc.z = fmaf(v.z, k, acc.z);
     acc.w = fmaf(v.w, k, acc.w);
   }
-  red[first][col] = acc;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) l += red_l[w];
-  if (threadIdx.x < kLanes) {
-    const float f = l == 0.f ? 0.f : gate_of(a, b, hq) / l;
-#pragma unroll
-    for (int r = 1; r < kRows; ++r) {
-      const float4 v = red[r][col];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
-    }
-    store2(out + 4 * col, acc.x * f, acc.y * f);
-    store2(out + 4 * col + 2, acc.z * f, acc.w * f);
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = (m + log2f(l)) * kLn2;
+  const float f = l == 0.f ? 0.f : gate_of(a, b, hq) / l;
+  store2(out + 4 * col, acc.x * f, acc.y * f);
+  store2(out + 4 * col + 2, acc.z * f, acc.w * f);
+  if (a.lse && col == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = (top + log2f(l)) * kLn2;
 }
 
 template <int D, bool FP8, int HT, typename TO>
@@ -728,7 +752,6 @@ zmoe_status launch(AttnArgs a, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.Hq);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(a.warps) * 4;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
