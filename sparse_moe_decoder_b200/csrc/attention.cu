@@ -61,6 +61,7 @@ struct AttnArgs {
   float* lse;             // [B, Hq] or null
   float* parts;           // [warps][2] of {m[H], l[H], O[H][D]}, H = 8 HT
   int warps;              // warps of the first kernel
+  int together;           // query heads of a group that a block of the second kernel joins
   unsigned int *errors, *timeouts;
 };
 
@@ -138,9 +139,8 @@ __host__ __device__ constexpr int part_floats() {
   return 8 * HT * (D + 2);
 }
 
-// How tiles of an 8-bit or a bf16 cache are read.  A tile's rows lie in shared memory as boxes of 128-byte lines
-// (two boxes of half rows where a row has 256 bytes, two rows a line where it has 64), each line's 16-byte chunks
-// exchanged by the line's number.
+// How tiles of an 8-bit or a bf16 cache are read.  A tile's rows lie in shared memory one after another as lines of
+// 128 bytes, each line's 16-byte chunks exchanged by the line's number (modulo 8).
 template <int D, bool FP8, int HT>
 struct Lay {
   static constexpr int esz = FP8 ? 1 : 2;
@@ -157,20 +157,24 @@ struct Lay {
   static constexpr int smem = kWarps * slots * slot + 1024;   // the ring starts on 1024 bytes
   static_assert(half % 1024 == 0 && tiles >= 1, "whole swizzle atoms");
 
-  // Chunk c of lane j's share of a key row, in 16-byte chunks of the row.
-  __device__ __forceinline__ static int k_chunk(int c, int j) { return row >= 128 ? (c >> 1) * 8 + 2 * j + (c & 1) : j; }
+  // Chunk c of lane j's share of a key row, in 16-byte chunks of the row: eight neighbouring lanes, which have two
+  // rows, reach all banks.
+  __device__ __forceinline__ static int k_chunk(int c, int j) {
+    if (row == 256) return (c >> 1) * 8 + (j >> 1) * 4 + (c & 1) * 2 + (j & 1);
+    return row == 128 ? 2 * j + c : j;
+  }
   // Byte `at` of token r's row within a tile.
   __device__ __forceinline__ static uint32_t place(int r, int at) {
-    const uint32_t x = row == 256 ? static_cast<uint32_t>((at >> 7) * 2048 + r * 128 + (at & 127))
-                                  : static_cast<uint32_t>(r * row + at);
+    const uint32_t x = static_cast<uint32_t>(r * row + at);
     return x ^ (((x >> 7) & 7u) << 4);
   }
 };
 
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+// A tile's rows from line `at` of the cache on.
+__device__ __forceinline__ void tma_lines(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int at) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(at)
       : "memory");
 }
 
@@ -298,11 +302,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
       if (line >= 0) have |= 1u << i;
       if (lane == 0 && i < here) {
         const int at = line >= 0 ? line : 0;   // any rows in place of none: these tokens do not count
-#pragma unroll
-        for (int c = 0; c < (L::row == 256 ? 2 : 1); ++c) {
-          tma_2d(dst + i * L::half + c * 2048, &kmap, full, c * 128, at);
-          tma_2d(dst + 4096 + i * L::half + c * 2048, &vmap, full, c * 128, at);
-        }
+        tma_lines(dst + i * L::half, &kmap, full, at);
+        tma_lines(dst + 4096 + i * L::half, &vmap, full, at);
       }
     }
     f_have |= have << (ahead * L::tiles);
@@ -618,8 +619,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
   }
 }
 
-// Joins the parts of the groups that were cut, one block per (sequence, query head), and writes the rows of empty
-// sequences.
+// Joins the parts of the groups that were cut and writes the rows of empty sequences.
 template <int D, int HT, typename TO>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
   constexpr int H = 8 * HT, kJoinWarps = kJoinThreads / 32, kLanes = D / 4, kRows = kJoinThreads / kLanes;
@@ -627,9 +627,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
   __shared__ long long start_of_b;
   __shared__ float red_m[kRows], red_l[kRows];
   __shared__ float4 red[kRows][kLanes];
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
-  const int hk = hq / a.G, in_group = hq - hk * a.G, gt = in_group / H, head = in_group - gt * H;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // D / 4 lanes have one head and every `ways`-th of its parts
+  const int per_group = (a.G + a.together - 1) / a.together, ways = kRows / a.together;
+  const int group = blockIdx.x / per_group, b = group / a.Hkv, hk = group - b * a.Hkv;
+  const int col = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+  const int in_group = (blockIdx.x - group * per_group) * a.together + row / ways;   // heads of a block share a tile
+  const int gt = in_group / H, head = in_group - gt * H, hq = hk * a.G + in_group, first = row % ways;
+  const bool real = in_group < a.G;
   const int units = a.Hkv * a.gtiles;
   const int per = (a.B + kJoinThreads - 1) / kJoinThreads, b_lo = threadIdx.x * per;
   const int b_hi = b_lo + per < a.B ? b_lo + per : a.B;
@@ -647,8 +651,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
   TO* out = static_cast<TO*>(a.out) + (static_cast<size_t>(b) * a.Hq + hq) * D;
   if (nt == 0) {   // the first kernel does not touch these rows, and it began behind what came before both
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int c = threadIdx.x * 2; c < D; c += kJoinThreads * 2) store2(out + c, 0.f, 0.f);
-    if (a.lse && threadIdx.x == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = __int_as_float(0xff800000);
+    if (real && first == 0) {
+      store2(out + 4 * col, 0.f, 0.f);
+      store2(out + 4 * col + 2, 0.f, 0.f);
+      if (a.lse && col == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = __int_as_float(0xff800000);
+    }
     return;
   }
   const long long p0 = start_of_b + static_cast<long long>(hk * a.gtiles + gt) * nt, p1 = p0 + nt;
@@ -660,17 +667,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
   auto part_of = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? first_slot : 0)) * part_floats<D, HT>(); };
   // every thread of the first kernel's grid is done, and its writes are visible, behind this line
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // D / 4 lanes take every kRows-th part, 8 of them in flight, with a running maximum
-  constexpr int kBatch = 8;
-  const int col = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
+  constexpr int kBatch = 8;   // parts in flight, with a running maximum
   float m = __int_as_float(0xff800000), l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = first; i0 < parts; i0 += kRows * kBatch) {
+  for (int i0 = first; i0 < parts; i0 += ways * kBatch) {
     float mi[kBatch], li[kBatch];
     float4 v[kBatch];
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
-      const int i = i0 + q * kRows;
+      const int i = i0 + q * ways;
       mi[q] = __int_as_float(0xff800000);
       if (i < parts) {
         const float* p = part_of(i);
@@ -689,7 +694,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
     m = top;
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
-      if (i0 + q * kRows < parts) {
+      if (i0 + q * ways < parts) {
         const float k = exp2f(mi[q] - zero);
         l = fmaf(li[q], k, l);
         acc.x = fmaf(v[q].x, k, acc.x);
@@ -699,34 +704,31 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
       }
     }
   }
-  red[first][col] = acc;
-  if (col == 0) {
-    red_m[first] = m;
-    red_l[first] = l;
+  if (ways > 1) {
+    red[row][col] = acc;
+    if (col == 0) {
+      red_m[row] = m;
+      red_l[row] = l;
+    }
+    __syncthreads();
+    if (first != 0) return;
+    for (int r = row + 1; r < row + ways && r - row < parts; ++r) {
+      const float other = red_m[r], top = fmaxf(m, other), zero = top == __int_as_float(0xff800000) ? 0.f : top;
+      const float k0 = exp2f(m - zero), k1 = exp2f(other - zero);
+      const float4 v = red[r][col];
+      m = top;
+      l = l * k0 + red_l[r] * k1;
+      acc.x = acc.x * k0 + v.x * k1;
+      acc.y = acc.y * k0 + v.y * k1;
+      acc.z = acc.z * k0 + v.z * k1;
+      acc.w = acc.w * k0 + v.w * k1;
+    }
   }
-  __syncthreads();
-  if (threadIdx.x >= kLanes) return;
-  float top = red_m[0];
-#pragma unroll
-  for (int r = 1; r < kRows; ++r) top = fmaxf(top, red_m[r]);
-  const float zero = top == __int_as_float(0xff800000) ? 0.f : top;
-  l = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (r >= parts) break;   // that row has no part
-    const float k = exp2f(red_m[r] - zero);
-    const float4 v = red[r][col];
-    l = fmaf(red_l[r], k, l);
-    acc.x = fmaf(v.x, k, acc.x);
-    acc.y = fmaf(v.y, k, acc.y);
-    acc.z = fmaf(v.z, k, acc.z);
-    acc.w = fmaf(v.w, k, acc.w);
-  }
+  if (!real) return;
   const float f = l == 0.f ? 0.f : gate_of(a, b, hq) / l;
   store2(out + 4 * col, acc.x * f, acc.y * f);
   store2(out + 4 * col + 2, acc.z * f, acc.w * f);
-  if (a.lse && col == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = (top + log2f(l)) * kLn2;
+  if (a.lse && col == 0) a.lse[static_cast<size_t>(b) * a.Hq + hq] = (m + log2f(l)) * kLn2;
 }
 
 template <int D, bool FP8, int HT, typename TO>
@@ -735,14 +737,14 @@ zmoe_status launch(AttnArgs a, cudaStream_t s) {
   static_assert(L::blocks * kWarps <= kMaxWarpsPerSm, "the workspace holds the warps' parts");
   const int blocks = num_sms() * L::blocks;
   a.warps = blocks * kWarps;
-  // the cache as lines of 128 bytes at least (two rows of an 8-bit cache of 64 columns), a box a tile or half of one
-  const cuuint64_t rows = static_cast<cuuint64_t>(a.n_pages) * a.Hkv * a.page_size;
-  const cuuint64_t dims[2] = {L::row < 128 ? 128 : L::row, rows * L::row / (L::row < 128 ? 128 : L::row)};
-  const cuuint64_t stride[1] = {dims[0]};
-  const cuuint32_t box[2] = {128, L::row < 128 ? 8 : 16};
+  // the cache as rows of one or two lines of 128 bytes (two rows of an 8-bit cache of 64 columns are a line)
+  const cuuint32_t lines = L::row == 256 ? 2 : 1, tall = L::row == 64 ? 8 : 16;
+  const cuuint64_t rows = static_cast<cuuint64_t>(a.n_pages) * a.Hkv * a.page_size * tall / 16;
+  const cuuint64_t dims[3] = {128, lines, rows}, stride[2] = {128, 128 * lines};
+  const cuuint32_t box[3] = {128, lines, tall};
   CUtensorMap km, vm;
-  if (!encode_map(&km, a.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dims, stride, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(&vm, a.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dims, stride, box, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!encode_map(&km, a.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, stride, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(&vm, a.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, stride, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return fail(ZMOE_ERR_CUDA, "zmoe_paged_attention: the cache's tensor map cannot be made");
   if (cudaFuncSetAttribute(attn_kernel<D, FP8, HT, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem) != cudaSuccess)
     return check_launch("zmoe_paged_attention: shared memory attribute");
@@ -750,7 +752,12 @@ zmoe_status launch(AttnArgs a, cudaStream_t s) {
   zmoe_status st = check_launch("zmoe_paged_attention");
   if (st != ZMOE_OK) return st;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.Hq);
+  // A block a head, unless they are more than run at once: then it takes up to 8 heads of a group.
+  a.together = 1;
+  while (static_cast<long long>(a.B) * a.Hkv * ((a.G + a.together - 1) / a.together) > 3LL * num_sms() &&
+         a.together < 8 && a.together < a.G)
+    a.together *= 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.Hkv * ((a.G + a.together - 1) / a.together));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
