@@ -84,6 +84,20 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Four E4M3 values -> two f16 pairs; exact.
+__device__ __forceinline__ void widen_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// 2^x, 0 below 2^-126.
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Tiles of 16 tokens of sequence b; a length beyond the table's pages is an error and cut to them.
 __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
   const int n = __ldg(a.lens + b);
@@ -365,17 +379,16 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest magnitude goes to [2^14, 2^15)
-        const int ex = top > 0.f && top < __int_as_float(0x7f800000) ? 14 - ilogbf(top) : 0;
-        if (r < HT) qs[r] = ldexpf(a.scale * kLog2e * __ldg(a.k_scale + hk), -ex);
+        // the largest magnitude goes to [2^14, 2^15), unless it is below 2^-86: such a query scores 0 anyway
+        const int bits = static_cast<int>(__float_as_uint(top) >> 23), ex = bits == 255 ? 0 : (bits < 41 ? 100 : 141 - bits);
+        const float up = __int_as_float((127 + ex) << 23);
+        if (r < HT) qs[r] = a.scale * kLog2e * __ldg(a.k_scale + hk) * __int_as_float((127 - ex) << 23);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float f[8];
           unpack_bf16x8(raw[c], f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = ldexpf(f[e], ex);
-          raw[c] = make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
-                              pack_f16x2(f[6], f[7]));
+          raw[c] = make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
+                              pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
         }
       }
 #pragma unroll
@@ -406,37 +419,45 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
       const uint32_t base = ring + slot * L::slot;
       // tokens of each tile that count
       int live[L::tiles];
+      bool full = true;
 #pragma unroll
       for (int i = 0; i < L::tiles; ++i) {
         const int left = t + i < t_end && ((f_have >> i) & 1u) ? n - (t + i) * 16 : 0;
         live[i] = left < 16 ? left : 16;
+        full = full && left >= 16;
       }
       float s[L::tiles][2][4];
 #pragma unroll
       for (int i = 0; i < L::tiles; ++i)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float(&d)[4] = s[i][r];
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = 0.f;
-          uint4 kr[L::kvecs];
+          for (int e = 0; e < 4; ++e) s[i][r][e] = 0.f;
+      // neighbouring products go to different sums
 #pragma unroll
-          for (int c = 0; c < L::kvecs; ++c)
-            kr[c] = lds128(base + i * L::half + L::place(g + 8 * r, L::k_chunk(c, j) * 16));
+      for (int c = 0; c < L::kvecs; ++c) {
+        uint4 kr[L::tiles][2];
 #pragma unroll
-          for (int c = 0; c < L::kvecs; ++c) {
-            const uint32_t w[4] = {kr[c].x, kr[c].y, kr[c].z, kr[c].w};
-            if (FP8) {
+        for (int i = 0; i < L::tiles; ++i)
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mma_f16(d, qf[4 * c + q], e4m3x2_to_f16x2(static_cast<uint16_t>(w[q] & 0xFFFFu)),
-                        e4m3x2_to_f16x2(static_cast<uint16_t>(w[q] >> 16)));
-            } else {
-              mma_bf16(d, qf[2 * c], w[0], w[1]);
-              mma_bf16(d, qf[2 * c + 1], w[2], w[3]);
+          for (int r = 0; r < 2; ++r)
+            kr[i][r] = lds128(base + i * L::half + L::place(g + 8 * r, L::k_chunk(c, j) * 16));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < L::tiles; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint4& v = kr[i][r];
+              if (FP8) {
+                uint32_t b0, b1;
+                widen_e4m3x4(q == 0 ? v.x : (q == 1 ? v.y : (q == 2 ? v.z : v.w)), b0, b1);
+                mma_f16(s[i][r], qf[4 * c + q], b0, b1);
+              } else if (q < 2) {
+                mma_bf16(s[i][r], qf[2 * c + q], q ? v.z : v.x, q ? v.w : v.y);
+              }
             }
-          }
-        }
+      }
       // softmax of the step: lane (g, j) has heads g (and g + 8), of each tile the tokens 8 r + 2 j and + 1
       uint32_t hi[L::tiles][HT][2], lo[L::tiles][HT][2];
 #pragma unroll
@@ -448,13 +469,13 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             z[i][e] = s[i][e >> 1][2 * h + (e & 1)] * qs[h];
-            if (8 * (e >> 1) + 2 * j + (e & 1) >= live[i]) z[i][e] = __int_as_float(0xff800000);
+            if (!full && 8 * (e >> 1) + 2 * j + (e & 1) >= live[i]) z[i][e] = __int_as_float(0xff800000);
             top = fmaxf(top, z[i][e]);
           }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         if (__any_sync(0xffffffffu, top > m[h])) {
-          const float keep = m[h] == top ? 1.f : exp2f(m[h] - top);   // top > -inf here, or m == top
+          const float keep = m[h] == top ? 1.f : pow2(m[h] - top);   // top > -inf here, or m == top
           l[h] *= keep;
           const float k0 = __shfl_sync(0xffffffffu, keep, 8 * j), k1 = __shfl_sync(0xffffffffu, keep, 8 * j + 4);
 #pragma unroll
@@ -472,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = exp2f(z[i][e] - zero);
+            p[e] = pow2(z[i][e] - zero);
             l[h] += p[e];
             p[e] *= kPScale;
           }
@@ -523,32 +544,40 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
               for (int w = 0; w < L::vwords; ++w) vr[r][w] = 0u;
             }
         }
+        // the column tiles of kSide words side by side: a tile's two products are apart from one another
+        constexpr int kSide = FP8 ? 2 : 4, kTiles = FP8 ? 2 * kSide : kSide;
 #pragma unroll
-        for (int w = 0; w < L::vwords; ++w) {
-          if (FP8) {
+        for (int w0 = 0; w0 < L::vwords; w0 += kSide) {
+          uint32_t va[kTiles][4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {   // columns 4 w + 2 half, + 1 of the lane's share
-              const uint32_t x = __byte_perm(vr[0][w], vr[1][w], half ? 0x7362 : 0x5140);
-              const uint32_t y = __byte_perm(vr[2][w], vr[3][w], half ? 0x7362 : 0x5140);
-              const uint32_t va[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(x & 0xFFFFu)),
-                                      e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16)),
-                                      e4m3x2_to_f16x2(static_cast<uint16_t>(y & 0xFFFFu)),
-                                      e4m3x2_to_f16x2(static_cast<uint16_t>(y >> 16))};
+          for (int k = 0; k < kSide; ++k) {
+            const int w = w0 + k;
+            if (FP8) {
 #pragma unroll
-              for (int h = 0; h < HT; ++h) {
-                mma_f16(o[h][2 * w + half], va, hi[i][h][0], hi[i][h][1]);
-                mma_f16(o[h][2 * w + half], va, lo[i][h][0], lo[i][h][1]);
+              for (int half = 0; half < 2; ++half) {   // columns 4 w + 2 half, + 1 of the lane's share
+                uint32_t(&t)[4] = va[(2 * k + half) % kTiles];
+                widen_e4m3x4(__byte_perm(vr[0][w], vr[1][w], half ? 0x7362 : 0x5140), t[0], t[1]);
+                widen_e4m3x4(__byte_perm(vr[2][w], vr[3][w], half ? 0x7362 : 0x5140), t[2], t[3]);
               }
-            }
-          } else {
-            const uint32_t va[4] = {__byte_perm(vr[0][w], vr[1][w], 0x5410), __byte_perm(vr[0][w], vr[1][w], 0x7632),
-                                    __byte_perm(vr[2][w], vr[3][w], 0x5410), __byte_perm(vr[2][w], vr[3][w], 0x7632)};
-#pragma unroll
-            for (int h = 0; h < HT; ++h) {
-              mma_bf16(o[h][w], va, hi[i][h][0], hi[i][h][1]);
-              mma_bf16(o[h][w], va, lo[i][h][0], lo[i][h][1]);
+            } else {
+              uint32_t(&t)[4] = va[k % kTiles];
+              t[0] = __byte_perm(vr[0][w], vr[1][w], 0x5410);
+              t[1] = __byte_perm(vr[0][w], vr[1][w], 0x7632);
+              t[2] = __byte_perm(vr[2][w], vr[3][w], 0x5410);
+              t[3] = __byte_perm(vr[2][w], vr[3][w], 0x7632);
             }
           }
+          const int o0 = FP8 ? 2 * w0 : w0;
+#pragma unroll
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+#pragma unroll
+              for (int k = 0; k < kTiles; ++k) {
+                const uint32_t p0 = term ? lo[i][h][0] : hi[i][h][0], p1 = term ? lo[i][h][1] : hi[i][h][1];
+                if (FP8) mma_f16(o[h][o0 + k], va[k], p0, p1);
+                else mma_bf16(o[h][o0 + k], va[k], p0, p1);
+              }
         }
       }
       // every lane has read the slot: it is filled again
