@@ -1,0 +1,169 @@
+"""The decoder's attention blocks at decode steps: a paged key-value cache, the block that reads and extends it, and
+the rules on the codebook logits that choose the next frame.
+
+ZONOS2 Technical Report digest, "method overview and architecture", item 5 (grouped-query attention with headwise
+gating, rotary positions, pre-norm blocks).  Everything on the device is preallocated and a step leaves no decision
+to the host but new pages (``PagedCache.reserve``), so a step may be captured into a CUDA graph once the pages are
+reserved.  The projections are zmoe_speaker_prefix's product W e, which streams the weights once per 8 tokens.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import List, Optional
+
+import torch
+
+from . import zmoe as Z
+
+
+@dataclass
+class AttentionWeights:
+    """One attention block: h <- h + W_o (sigmoid(W_gate x) * attention(W_qkv x)), x = RMSNorm(h) * gamma.
+
+    w_qkv [(Hq + 2 Hkv) D, d]: the queries', keys' and values' rows one after another; w_o [d, Hq D]; w_gate [Hq, d]
+    or None (no gates); gamma f32 [d]; q_gamma, k_gamma f32 [D] or None (no query or key norm)."""
+
+    w_qkv: torch.Tensor
+    w_o: torch.Tensor
+    gamma: torch.Tensor
+    Hq: int
+    Hkv: int
+    w_gate: Optional[torch.Tensor] = None
+    q_gamma: Optional[torch.Tensor] = None
+    k_gamma: Optional[torch.Tensor] = None
+
+    @property
+    def D(self) -> int:
+        return self.w_qkv.shape[0] // (self.Hq + 2 * self.Hkv)
+
+
+class PagedCache:
+    """Keys and values of ``n_seqs`` sequences in pages, for ``n_layers`` layers that share one page table.
+
+    dtype torch.bfloat16, or torch.uint8 for E4M3 codes with k_scale, v_scale f32 [n_layers, Hkv].  Pages are handed
+    out by ``reserve`` and taken back by ``release``; ``advance`` gives every sequence its next position."""
+
+    def __init__(self, n_layers: int, n_seqs: int, max_len: int, Hkv: int, D: int, page_size: int = 16,
+                 n_pages: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None, device="cuda"):
+        if page_size < 16 or page_size % 16:
+            raise ValueError("page_size must be a multiple of 16")
+        if (dtype == torch.uint8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("an E4M3 cache (uint8), and no other, has k_scale and v_scale")
+        self.page_size, self.n_seqs, self.max_len = page_size, n_seqs, max_len
+        cols = -(-max_len // page_size)
+        self.n_pages = n_seqs * cols if n_pages is None else n_pages
+        shape = (n_layers, self.n_pages, Hkv, page_size, D)
+        self.k, self.v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.table = torch.full((n_seqs, cols), -1, dtype=torch.int32, device=device)
+        self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=device)   # cached tokens
+        self.pos = torch.zeros(n_seqs, dtype=torch.int32, device=device)    # the step's positions
+        self.free: List[int] = list(range(self.n_pages - 1, -1, -1))
+        self.pages: List[List[int]] = [[] for _ in range(n_seqs)]
+
+    def reserve(self, length: int, seq: Optional[int] = None) -> None:
+        """Pages for the first ``length`` tokens of sequence ``seq`` (None: of every sequence)."""
+        if length > self.max_len:
+            raise ValueError(f"{length} tokens in a cache of {self.max_len}")
+        need = -(-length // self.page_size)
+        for s in range(self.n_seqs) if seq is None else (seq,):
+            have = len(self.pages[s])
+            if need <= have:
+                continue
+            if need - have > len(self.free):
+                raise RuntimeError(f"the cache is out of pages: sequence {s} needs {need - have}, {len(self.free)} are free")
+            new = [self.free.pop() for _ in range(need - have)]
+            self.pages[s] += new
+            self.table[s, have:need] = torch.tensor(new, dtype=torch.int32)
+
+    def release(self, seq: int) -> None:
+        """Takes a sequence's pages back; it starts again at position 0."""
+        self.free += reversed(self.pages[seq])
+        self.pages[seq] = []
+        self.table[seq].fill_(-1)
+        self.lens[seq].zero_()
+
+    def advance(self, stream=None) -> None:
+        """One more token for every sequence: its position in ``pos``, its new length in ``lens``.  A position
+        without a reserved page counts a device error when the token is stored, and the token is lost."""
+        with torch.cuda.stream(stream):
+            self.pos.copy_(self.lens)
+            self.lens.add_(1)
+
+    def layer(self, i: int) -> dict:
+        """The cache arguments of zmoe_kv_append and zmoe_paged_attention for layer ``i``."""
+        return dict(k_cache=self.k[i], v_cache=self.v[i], page_table=self.table,
+                    k_scale=None if self.k_scale is None else self.k_scale[i],
+                    v_scale=None if self.v_scale is None else self.v_scale[i])
+
+
+class AttentionRunner:
+    """Preallocated buffers of one attention block shape for T sequences."""
+
+    def __init__(self, T: int, d: int, Hq: int, Hkv: int, D: int, inv_freq: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, device="cuda"):
+        dev = torch.device(device)
+        self.Hq, self.Hkv, self.D, self.inv_freq, self.interleaved = Hq, Hkv, D, inv_freq, interleaved
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.x = torch.empty((T, d), **f32)
+        qkv = self.qkv = torch.empty((T, (Hq + 2 * Hkv) * D), **f32)
+        self.q_in = qkv[:, :Hq * D].unflatten(1, (Hq, D))
+        self.k_in = qkv[:, Hq * D:(Hq + Hkv) * D].unflatten(1, (Hkv, D))
+        self.v_in = qkv[:, (Hq + Hkv) * D:].unflatten(1, (Hkv, D))
+        self.q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        self.gate = torch.empty((T, Hq), **f32)
+        self.o = torch.empty((T, Hq, D), **f32)
+        self.delta = torch.empty((T, d), **f32)
+        n = Z.zmoe_paged_attention_workspace_size(T, Hq, Hkv, D)
+        self.workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+
+    def run(self, h: torch.Tensor, W: AttentionWeights, cache: PagedCache, layer: int, eps: float = 1e-6,
+            gamma_next: Optional[torch.Tensor] = None, x_next: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """h <- h + the block's output for the token at cache.pos of each sequence, in place; h f32 [T, d].
+
+        With ``gamma_next``, x_next [T, d] receives RMSNorm(h) * gamma_next of the new h (the next block's input)."""
+        c = cache.layer(layer)
+        Z.zmoe_add_rmsnorm(h, W.gamma, eps=eps, outs=dict(x=self.x), stream=stream)
+        Z.zmoe_speaker_prefix(self.x, W.w_qkv, out=self.qkv, stream=stream)
+        if W.w_gate is not None:
+            Z.zmoe_speaker_prefix(self.x, W.w_gate, out=self.gate, stream=stream)
+        Z.zmoe_kv_append(self.k_in, self.v_in, cache.pos, q=self.q_in, inv_freq=self.inv_freq,
+                         interleaved=self.interleaved, q_gamma=W.q_gamma, k_gamma=W.k_gamma, eps=eps, q_out=self.q,
+                         stream=stream, **c)
+        Z.zmoe_paged_attention(self.q, lens=cache.lens, gate=self.gate if W.w_gate is not None else None, out=self.o,
+                               workspace=self.workspace, stream=stream, **c)
+        Z.zmoe_speaker_prefix(self.o.flatten(1), W.w_o, out=self.delta, stream=stream)
+        outs = dict(h=h)
+        if gamma_next is not None:
+            outs["x"] = x_next
+        Z.zmoe_add_rmsnorm(h, W.gamma if gamma_next is None else gamma_next, self.delta, eps=eps, outs=outs, stream=stream)
+        return h
+
+
+class LogitRules:
+    """What zmoe_adjust_logits does to the heads' logits: penalties by the last ``window`` frames of each of T streams,
+    bias f32 [N, V], mask int32 [T, N, ceil(V / 32)] of allowed ids (bits).  repetition, presence, frequency: f32 [T]."""
+
+    def __init__(self, T: int, N: int, window: int, repetition: Optional[torch.Tensor] = None,
+                 presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                 bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None, device="cuda"):
+        if window < 1:
+            raise ValueError("window must be at least 1")
+        self.repetition, self.presence, self.frequency, self.bias, self.mask = repetition, presence, frequency, bias, mask
+        self.history = torch.full((T, window, N), -1, dtype=torch.int32, device=device)
+        self.hist_lens = torch.zeros(T, dtype=torch.int32, device=device)
+        self.slot = torch.zeros(1, dtype=torch.int64, device=device)   # where the next frame goes; the order is free
+
+    def choose(self, logits: torch.Tensor, ids: torch.Tensor, stream=None) -> None:
+        """Adjusts logits [T, N, V] in place and writes the greedy frame to ids int32 [T, N]."""
+        Z.zmoe_adjust_logits(logits, self.history, self.hist_lens, self.repetition, self.presence, self.frequency,
+                             self.bias, self.mask, out=logits, ids=ids, stream=stream)
+
+    def remember(self, ids: torch.Tensor, stream=None) -> None:
+        """Adds the frame ids [T, N] to the history, in place of the oldest when the window is full."""
+        window = self.history.shape[1]
+        with torch.cuda.stream(stream):
+            self.history.index_copy_(1, self.slot, ids.unsqueeze(1))
+            self.slot.add_(1).remainder_(window)
+            self.hist_lens.add_(1).clamp_(max=window)

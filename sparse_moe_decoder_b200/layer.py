@@ -20,6 +20,7 @@ from typing import List, Optional
 import torch
 
 from . import zmoe as Z
+from .attention import AttentionRunner, AttentionWeights, LogitRules, PagedCache
 
 
 @dataclass
@@ -155,11 +156,19 @@ class MoELayerRunner:
 
 class DecodeStack:
     """Embedding sum + RMSNorm, then L pre-norm residual MoE layers, for T tokens per step; with head
-    weights, also the codebook heads and the greedy next frame (``next_ids``)."""
+    weights, also the codebook heads and the greedy next frame (``next_ids``).
+
+    With ``attention`` (a block for each layer, or None where a layer has none) and the ``cache`` of its T sequences,
+    each layer is the decoder's: the attention block, then the MoE layer; every step adds a token to each sequence
+    (``cache.reserve`` gives out the pages).  inv_freq f64 [rotary_dim / 2] and ``interleaved``: zmoe_kv_append's.
+    With ``rules`` the heads' logits (kept in ``logits``) are adjusted before the next frame is chosen, and the frame
+    joins the rules' history."""
 
     def __init__(self, tables: torch.Tensor, gamma0: torch.Tensor, layers: List[MoEWeights], eps: float = 1e-6,
                  T: int = 1, w_heads: Optional[torch.Tensor] = None, gamma_out: Optional[torch.Tensor] = None,
-                 persistent: Optional[bool] = None):
+                 persistent: Optional[bool] = None, attention: Optional[List[Optional[AttentionWeights]]] = None,
+                 cache: Optional[PagedCache] = None, inv_freq: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, rules: Optional[LogitRules] = None):
         self.tables, self.gamma0, self.layers, self.eps, self.T = tables, gamma0, layers, eps, T
         L0 = layers[0]
         dev = tables.device
@@ -173,6 +182,22 @@ class DecodeStack:
         self.head_x = torch.empty((T, L0.d), dtype=L0.dtype, device=dev)
         self.head_ws = torch.empty(max(int(Z.lib().zmoe_output_heads_workspace_size(T, tables.shape[0])), 16),
                                    dtype=torch.uint8, device=dev) if w_heads is not None else None
+        if attention is not None:
+            if persistent:
+                raise ValueError("zmoe_decode_stack has no attention blocks")
+            if cache is None or len(attention) != len(layers) or cache.n_seqs != T:
+                raise ValueError("attention needs an entry for each layer and a cache of T sequences")
+            if any(L.gamma is None for L in layers):
+                raise ValueError("a layer behind an attention block needs its pre-norm gain")
+            persistent = False
+        if rules is not None and w_heads is None:
+            raise ValueError("rules need the heads")
+        self.attention, self.cache, self.rules = attention, cache, rules
+        self.att_runners = {}
+        for A in attention or []:
+            if A is not None and (A.Hq, A.Hkv, A.D) not in self.att_runners:
+                self.att_runners[A.Hq, A.Hkv, A.D] = AttentionRunner(T, L0.d, A.Hq, A.Hkv, A.D, inv_freq, interleaved, dev)
+        self.logits = torch.empty((T, *w_heads.shape[:2]), dtype=torch.float32, device=dev) if rules is not None else None
         self.record_inputs = False
         self.layer_inputs: List[torch.Tensor] = []
         self.layer_h: List[torch.Tensor] = []
@@ -210,13 +235,23 @@ class DecodeStack:
         Z.zmoe_embed_sum_rmsnorm(self.ids, self.tables, self.gamma0, self.eps, out=self.h, stream=stream)
         if self.record_inputs:
             self.layer_inputs, self.layer_h, self.layer_idx = [], [], []
-        for L in self.layers:
+        if self.attention is not None:
+            self.cache.advance(stream)
+        for l, L in enumerate(self.layers):
             R = self.runners[(L.E, L.k)]
+            A = self.attention[l] if self.attention is not None else None
+            if A is not None:
+                # h <- h + attention(RMSNorm(h)), and the MoE layer's x = RMSNorm(h) * gamma with it
+                self.att_runners[A.Hq, A.Hkv, A.D].run(self.h, A, self.cache, l, self.eps, gamma_next=L.gamma,
+                                                       x_next=self.x, stream=stream)
             if self.record_inputs:
                 self.layer_h.append(self.h.clone())
-            # h <- h + MoE(RMSNorm(h) * gamma): one zmoe_moe_layer call, in place
-            R.run(None, L, residual=self.h, out=self.h, stream=stream, gamma=L.gamma, eps=self.eps,
-                  x_norm=self.x if self.record_inputs else None)
+            if A is not None:
+                R.run(self.x, L, residual=self.h, out=self.h, stream=stream)
+            else:
+                # h <- h + MoE(RMSNorm(h) * gamma): one zmoe_moe_layer call, in place
+                R.run(None, L, residual=self.h, out=self.h, stream=stream, gamma=L.gamma, eps=self.eps,
+                      x_norm=self.x if self.record_inputs else None)
             if self.record_inputs:
                 self.layer_inputs.append(self.x.clone())
                 self.layer_idx.append(R.idx.clone())
@@ -226,8 +261,13 @@ class DecodeStack:
     def _heads(self, stream=None):
         if self.w_heads is not None:
             outs = dict(ids=self.next_ids, x=self.head_x) if self.record_inputs else dict(ids=self.next_ids)
+            if self.rules is not None:
+                outs["logits"] = self.logits
             Z.zmoe_output_heads(self.h, self.w_heads, self.gamma_out, self.eps, outs=outs, workspace=self.head_ws,
                                 stream=stream)
+            if self.rules is not None:
+                self.rules.choose(self.logits, self.next_ids, stream)
+                self.rules.remember(self.next_ids, stream)
 
 
 def stack_from_bits(tables_bits, gamma0, layer_small, expert_bits, n_layers: int, E: int, d: int, f: int,

@@ -1,0 +1,54 @@
+"""The decoder's host side on the CPU: pages given out and taken back, positions, and the window of frames."""
+import pytest
+import torch
+
+from sparse_moe_decoder_b200 import LogitRules, PagedCache
+
+
+def test_pages_are_given_out_once_and_taken_back():
+    c = PagedCache(2, 3, 50, 1, 64, 16, n_pages=7, device="cpu")
+    assert c.table.shape == (3, 4) and bool((c.table == -1).all())
+    c.reserve(17)
+    c.reserve(16, seq=0)                       # no more than it has
+    assert [len(p) for p in c.pages] == [2, 2, 2]
+    used = c.table[c.table >= 0].tolist()
+    assert len(used) == len(set(used)) == 6 and all(0 <= x < 7 for x in used)
+    c.reserve(33, seq=1)
+    assert c.free == [] and c.table[1, :3].tolist() == c.pages[1]
+    with pytest.raises(RuntimeError, match="out of pages"):
+        c.reserve(33, seq=2)
+    assert [len(p) for p in c.pages] == [2, 3, 2]      # the refused call took nothing
+    c.advance()
+    c.advance()
+    assert c.lens.tolist() == [2, 2, 2] and c.pos.tolist() == [1, 1, 1]
+    mine = c.pages[1]
+    c.release(1)
+    assert sorted(c.free) == sorted(mine) and bool((c.table[1] == -1).all()) and c.lens.tolist() == [2, 0, 2]
+    c.reserve(40, seq=2)
+    assert c.table[2, 2].item() in mine
+
+
+def test_a_layer_is_a_view_of_the_cache():
+    s = torch.ones(2, 1)
+    c = PagedCache(2, 1, 16, 1, 64, 16, dtype=torch.uint8, k_scale=s, v_scale=2 * s, device="cpu")
+    a = c.layer(1)
+    assert a["k_cache"].data_ptr() == c.k[1].data_ptr() and a["v_scale"].tolist() == [2.0] and a["page_table"] is c.table
+
+
+def test_cache_refusals():
+    for kw in (dict(page_size=8), dict(page_size=24), dict(dtype=torch.uint8), dict(k_scale=torch.ones(1, 1)),
+               dict(dtype=torch.uint8, k_scale=torch.ones(1, 1))):
+        with pytest.raises(ValueError):
+            PagedCache(1, 1, 16, 1, 64, device="cpu", **kw)
+    with pytest.raises(ValueError):
+        PagedCache(1, 1, 16, 1, 64, device="cpu").reserve(17)
+
+
+def test_the_window_keeps_the_last_frames():
+    r = LogitRules(2, 3, 4, device="cpu")
+    for i in range(6):
+        r.remember(torch.full((2, 3), i, dtype=torch.int32))
+        assert r.hist_lens.tolist() == [min(i + 1, 4)] * 2
+    assert sorted(r.history[1, :, 2].tolist()) == [2, 3, 4, 5]
+    with pytest.raises(ValueError):
+        LogitRules(1, 1, 0, device="cpu")
