@@ -5,7 +5,9 @@
 Each .cu file under csrc/ is compiled to an object with
 ``-gencode arch=compute_100a,code=sm_100a -O3 -lineinfo`` and the objects are linked
 into ``sparse_moe_decoder_b200/libzmoe.so`` with the static CUDA runtime.  An object is
-rebuilt only when its source or a header is newer.
+rebuilt only when its source or a header is newer.  The compiled calls of the decode-step
+operators (csrc/binding.cpp, g++ against torch's and Python's headers) become ``_binding.so``
+beside it.
 """
 from __future__ import annotations
 
@@ -22,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzmoe.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -61,7 +64,32 @@ def build(verbose: bool = False, force: bool = False, extra: list[str] | None = 
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+    build_binding(verbose, force)
     return LIB
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    """_binding.so: a CPython module that links to libzmoe.so and to the torch it is built against."""
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = max(os.path.getmtime(src), _newest_header())
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           "-isystem", os.path.join(base, "include"), "-isystem", os.path.join(base, "include/torch/csrc/api/include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), src, "-o", BINDING,
+           "-L" + PKG, "-lzmoe", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return BINDING
 
 
 def main(argv=None) -> int:

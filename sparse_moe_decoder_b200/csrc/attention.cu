@@ -24,11 +24,12 @@
 // in the workspace, and a second kernel, launched to start early (programmatic dependent launch), joins them in a
 // fixed order.
 //
-// P is split into two 16-bit terms, P = P_hi + P_lo (the second product runs twice): one bf16 term alone would
-// cost 2^-9 of every weight.  P_hi is cut, not rounded, so that P_lo is never negative, and P_lo is at least 2^-126
-// where P is not 0: an infinite value then meets two positive weights and stays an infinity, as in the formula.
-// An 8-bit cache is expanded to f16, exactly; its queries are scaled by a power of two per head to use f16's range,
-// and so is P.
+// P is split into 16-bit terms, P = P_1 + P_2 (+ P_3), and the second product runs for each: one bf16 term alone would
+// cost 2^-9 of every weight.  Two bf16 terms leave 2^-16 of it, which a bf16 output does not show; an f32 output takes
+// a third, and an f16 pair (8-bit cache) has 22 bits.  The bf16 terms are cut, not rounded, so that none is negative,
+// and are at least 2^-126 where P is not 0: an infinite value then meets positive weights only and stays an infinity,
+// as in the formula.  An 8-bit cache is expanded to f16, exactly; its queries are scaled by a power of two per head to
+// use f16's range, and so is P.
 #include "sm100_ptx.cuh"
 #include "vectors.cuh"
 
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
     attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a) {
   using L = Lay<D, FP8, HT>;
   constexpr int H = 8 * HT;
+  constexpr int kTerms = !FP8 && sizeof(TO) == 4 ? 3 : 2;
   constexpr float kPScale = FP8 ? 32768.f : 1.f;   // f16 holds P in [0, 2^15]: weights down to 2^-39 survive
   extern __shared__ unsigned char ring_raw[];
   __shared__ uint64_t bars[kWarps][L::slots];
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
             }
       }
       // softmax of the step: lane (g, j) has heads g (and g + 8), of each tile the tokens 8 r + 2 j and + 1
-      uint32_t hi[L::tiles][HT][2], lo[L::tiles][HT][2];
+      uint32_t pt[L::tiles][HT][kTerms][2];   // P's terms
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
         float z[L::tiles][4];
@@ -499,17 +501,26 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
           }
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
+            const float p0 = p[2 * r], p1 = p[2 * r + 1];
             if (FP8) {
-              hi[i][h][r] = pack_f16x2(p[2 * r], p[2 * r + 1]);
-              const __half2 t2 = *reinterpret_cast<const __half2*>(&hi[i][h][r]);
-              lo[i][h][r] = pack_f16x2(p[2 * r] - __low2float(t2), p[2 * r + 1] - __high2float(t2));
+              const uint32_t w = pack_f16x2(p0, p1);
+              const __half2 t2 = *reinterpret_cast<const __half2*>(&w);
+              pt[i][h][0][r] = w;
+              pt[i][h][1][r] = pack_f16x2(p0 - __low2float(t2), p1 - __high2float(t2));
             } else {
-              constexpr float kLeast = 1.17549435e-38f;   // 2^-126
-              const uint32_t x = __float_as_uint(p[2 * r]), y = __float_as_uint(p[2 * r + 1]);
-              hi[i][h][r] = __byte_perm(x, y, 0x7632);
-              lo[i][h][r] = round_bf16x2(
-                  fmaxf(p[2 * r] - __uint_as_float(x & 0xFFFF0000u), fminf(p[2 * r], kLeast)),
-                  fmaxf(p[2 * r + 1] - __uint_as_float(y & 0xFFFF0000u), fminf(p[2 * r + 1], kLeast)));
+              const float least0 = fminf(p0, 1.17549435e-38f), least1 = fminf(p1, 1.17549435e-38f);   // 2^-126
+              float r0 = p0, r1 = p1;   // what is left of P
+#pragma unroll
+              for (int t = 0; t < kTerms; ++t) {
+                if (t == kTerms - 1) {
+                  pt[i][h][t][r] = round_bf16x2(r0, r1);
+                } else {
+                  const uint32_t x = __float_as_uint(r0), y = __float_as_uint(r1);
+                  pt[i][h][t][r] = __byte_perm(x, y, 0x7632);
+                  r0 = fmaxf(r0 - __uint_as_float(x & 0xFFFF0000u), least0);
+                  r1 = fmaxf(r1 - __uint_as_float(y & 0xFFFF0000u), least1);
+                }
+              }
             }
           }
         }
@@ -544,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
               for (int w = 0; w < L::vwords; ++w) vr[r][w] = 0u;
             }
         }
-        // the column tiles of kSide words side by side: a tile's two products are apart from one another
+        // the column tiles of kSide words side by side: a tile's products are apart from one another
         constexpr int kSide = FP8 ? 2 : 4, kTiles = FP8 ? 2 * kSide : kSide;
 #pragma unroll
         for (int w0 = 0; w0 < L::vwords; w0 += kSide) {
@@ -569,14 +580,13 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
           }
           const int o0 = FP8 ? 2 * w0 : w0;
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
+          for (int t = 0; t < kTerms; ++t)
 #pragma unroll
             for (int h = 0; h < HT; ++h)
 #pragma unroll
               for (int k = 0; k < kTiles; ++k) {
-                const uint32_t p0 = term ? lo[i][h][0] : hi[i][h][0], p1 = term ? lo[i][h][1] : hi[i][h][1];
-                if (FP8) mma_f16(o[h][o0 + k], va[k], p0, p1);
-                else mma_bf16(o[h][o0 + k], va[k], p0, p1);
+                if (FP8) mma_f16(o[h][o0 + k], va[k], pt[i][h][t][0], pt[i][h][t][1]);
+                else mma_bf16(o[h][o0 + k], va[k], pt[i][h][t][0], pt[i][h][t][1]);
               }
         }
       }

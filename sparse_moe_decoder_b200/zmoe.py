@@ -90,6 +90,7 @@ class ZmoeError(RuntimeError):
 
 
 _lib: Optional[ctypes.CDLL] = None
+_binding = None   # the compiled calls, once loaded
 
 
 def lib() -> ctypes.CDLL:
@@ -579,17 +580,17 @@ def zmoe_decode_stack(layers, h: torch.Tensor, eps: float = 1e-6, ids: Optional[
     return h
 
 
-def _at(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int) -> Optional[int]:
-    """The address of a contiguous CUDA tensor of exactly this type (None: any), shape (None: any) and device."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or (t.dtype is not dtype and dtype is not None) or not t.is_contiguous() or \
-            t.get_device() != dev or (shape is not None and t.shape != shape):
-        _need(t, name, dtype)
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        raise ValueError(f"{name} is on {t.device}, the call's tensors are on cuda:{dev}")
-    return t.data_ptr()
+def _calls():
+    """The compiled argument checks and calls (csrc/binding.cpp) of the decode-step operators."""
+    global _binding
+    if _binding is None:
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError("the compiled binding cannot be loaded; build it with "
+                              f"`python -m sparse_moe_decoder_b200.build` ({e})") from e
+        _binding = module
+    return _binding
 
 
 def _out(shape, dtype, dev: int, stream, shared: bool = True) -> torch.Tensor:
@@ -604,26 +605,11 @@ def _out(shape, dtype, dev: int, stream, shared: bool = True) -> torch.Tensor:
     return t
 
 
-def _call(name: str, dev: int, stream, *args) -> None:
-    """One C call on the device of its tensors and on its current stream, or on `stream`."""
-    fn = getattr(_lib or lib(), name)
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        _on_device(stream, dev)
-        raw = stream.cuda_stream
-    if dev == torch.cuda.current_device():
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status:
-        _check(status, name)
-
-
-def _on_device(stream, dev: int) -> None:
-    if stream is not None and stream.device.index != dev:
-        raise ValueError(f"the stream is on {stream.device}, the call's tensors are on cuda:{dev}")
+def _empty_for(t: torch.Tensor, name: str, shape, dtype, stream) -> torch.Tensor:
+    """A new output for a call whose tensor `t` is an argument."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return _out(shape, dtype, t.get_device(), stream)
 
 
 def zmoe_add_rmsnorm(h: torch.Tensor, gamma: torch.Tensor, delta: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -634,53 +620,20 @@ def zmoe_add_rmsnorm(h: torch.Tensor, gamma: torch.Tensor, delta: Optional[torch
     Returns dict(h=, x=, codes=uint8, scales=f32 [T, 1] or [T, d / 128]).  With ``outs`` the outputs are the
     preallocated tensors it holds under those names (h may be ``h`` itself) and nothing else is computed;
     without it h (when there is a delta), x and, with want_codes, the codes are allocated."""
-    _need(h, "h", None, 2)
-    T, d = shape = h.shape
-    dev = h.get_device()
-    _on_device(stream, dev)
-    scales_shape = (T, d // group if group else 1)
     if outs is None:
-        outs = dict(x=_out(shape, out_dtype, dev, stream))
+        _need(h, "h", None, 2)
+        T, d = shape = h.shape
+        outs = dict(x=_empty_for(h, "h", shape, out_dtype, stream))
         if delta is not None:
-            outs["h"] = _out(shape, h.dtype, dev, stream)
+            outs["h"] = _empty_for(h, "h", shape, h.dtype, stream)
         if want_codes:
-            outs["codes"] = _out(shape, torch.uint8, dev, stream)
-            outs["scales"] = _out(scales_shape, torch.float32, dev, stream)
+            outs["codes"] = _empty_for(h, "h", shape, torch.uint8, stream)
+            outs["scales"] = _empty_for(h, "h", (T, d // group if group else 1), torch.float32, stream)
     ho, x, codes, scales = outs.get("h"), outs.get("x"), outs.get("codes"), outs.get("scales")
-    if x is not None:
-        out_dtype = x.dtype
-    _call("zmoe_add_rmsnorm", dev, stream, h.data_ptr(), _dtype_code(h.dtype), _at(delta, "delta", None, shape, dev),
-          ZMOE_F32 if delta is None else _dtype_code(delta.dtype), _at(gamma, "gamma", torch.float32, (d,), dev), eps,
-          T, d, _at(ho, "outs['h']", h.dtype, shape, dev), _at(x, "outs['x']", None, shape, dev),
-          _dtype_code(out_dtype), _at(codes, "outs['codes']", torch.uint8, shape, dev),
-          _at(scales, "outs['scales']", torch.float32, scales_shape, dev), group)
+    status = (_binding or _calls()).add_rmsnorm(h, gamma, delta, eps, ho, x, None, codes, scales, group, stream)
+    if status:
+        _check(status, "zmoe_add_rmsnorm")
     return dict(h=ho, x=x, codes=codes, scales=scales)
-
-
-def _cache_dims(k_cache: torch.Tensor):
-    """(kv dtype code, device, n_pages, Hkv, page_size, D) of a paged cache."""
-    _need(k_cache, "k_cache", None, 4)
-    if k_cache.dtype is torch.bfloat16:
-        return (ZMOE_BF16, k_cache.get_device(), *k_cache.shape)
-    if k_cache.dtype is torch.uint8:
-        return (ZMOE_E4M3, k_cache.get_device(), *k_cache.shape)
-    raise TypeError(f"k_cache must be bfloat16 or uint8 (E4M3 codes), got {k_cache.dtype}")
-
-
-def _heads(t: torch.Tensor, name: str, T: int, H: int, D: int, dtype, dev: int) -> int:
-    """A [T, H, D] view whose heads are contiguous; returns the elements between its tokens."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (T, H, D):
-        raise ValueError(f"{name} must have shape {(T, H, D)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{dev}")
-    s0, s1, s2 = t.stride()
-    if T and ((D > 1 and s2 != 1) or (H > 1 and s1 != D)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
-    return s0 if T > 1 else H * D
 
 
 def zmoe_kv_append(k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -694,33 +647,15 @@ def zmoe_kv_append(k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, k_cache:
     q [T, Hq, D], k, v [T, Hkv, D]: f32 or bf16 views of a packed projection; pos int32 [T]; seq int32 [T] (None:
     token t is sequence t's; negative: padding); k_cache, v_cache [n_pages, Hkv, page_size, D] bf16, or uint8
     E4M3 codes with k_scale, v_scale f32 [Hkv]; page_table int32 [n_seqs, max_pages]; inv_freq f64 [rotary_dim / 2]."""
-    kv, dev, n_pages, Hkv, page_size, D = _cache_dims(k_cache)
-    _on_device(stream, dev)
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must have 3 dims")
-    T, dt = k.shape[0], k.dtype
-    ks, vs = _heads(k, "k", T, Hkv, D, dt, dev), _heads(v, "v", T, Hkv, D, dt, dev)
-    Hq = qs = 0
-    if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise ValueError("q must have 3 dims")
-        Hq = q.shape[1]
-        qs = _heads(q, "q", T, Hq, D, dt, dev)
-        if q_out is None:
-            q_out = _out((T, Hq, D), torch.bfloat16, dev, stream)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    table = _at(page_table, "page_table", torch.int32, None, dev)
-    n_seqs, max_pages = page_table.shape
-    _call("zmoe_kv_append", dev, stream, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          _dtype_code(dt), qs, ks, vs, _at(seq, "seq", torch.int32, (T,), dev), _at(pos, "pos", torch.int32, (T,), dev),
-          _at(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev) if rot else None, rot, interleaved,
-          _at(q_gamma, "q_gamma", torch.float32, (D,), dev), _at(k_gamma, "k_gamma", torch.float32, (D,), dev), eps, T,
-          Hq, Hkv, D, _at(q_out, "q_out", torch.bfloat16, (T, Hq, D), dev), k_cache.data_ptr(),
-          _at(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev), kv,
-          _at(k_scale, "k_scale", torch.float32, (Hkv,), dev), _at(v_scale, "v_scale", torch.float32, (Hkv,), dev),
-          table, n_seqs, max_pages, n_pages, page_size)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    elif q_out is None:
+        q_out = _empty_for(q, "q", q.shape, torch.bfloat16, stream)
+    status = (_binding or _calls()).kv_append(k, v, pos, k_cache, v_cache, page_table, q, seq, inv_freq, interleaved,
+                                              q_gamma, k_gamma, eps, k_scale, v_scale, q_out, stream)
+    if status:
+        _check(status, "zmoe_kv_append")
     return q_out
 
 
@@ -738,28 +673,17 @@ def zmoe_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
 
     page_table int32 [B, max_pages], lens int32 [B]; scale defaults to 1 / sqrt(D); gate f32 [B, Hq]: the output
     times sigmoid(gate); lse f32 [B, Hq] receives the log of the sum of exp(scores)."""
-    kv, dev, n_pages, Hkv, page_size, D = _cache_dims(k_cache)
-    _on_device(stream, dev)
-    _need(q, "q", torch.bfloat16, 3)
-    B, Hq, _ = q.shape
-    shape = (B, Hq, D)
-    if page_table is None or lens is None:
-        raise ValueError("page_table and lens are needed")
-    table = _at(page_table, "page_table", torch.int32, None, dev)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table must have shape [{B}, max_pages], got {tuple(page_table.shape)}")
     if out is None:
-        out = _out(shape, out_dtype, dev, stream)
+        out = _empty_for(q, "q", q.shape, out_dtype, stream)
     if workspace is None:
-        n = zmoe_paged_attention_workspace_size(B, Hq, Hkv, D)
-        workspace = _out((max(n, 16),), torch.uint8, dev, stream, shared=False)
-    _call("zmoe_paged_attention", dev, stream, _at(q, "q", torch.bfloat16, shape, dev), k_cache.data_ptr(),
-          _at(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev), kv,
-          _at(k_scale, "k_scale", torch.float32, (Hkv,), dev), _at(v_scale, "v_scale", torch.float32, (Hkv,), dev),
-          table, _at(lens, "lens", torch.int32, (B,), dev), _at(gate, "gate", torch.float32, (B, Hq), dev),
-          D ** -0.5 if scale is None else scale, B, Hq, Hkv, D, page_table.shape[1], n_pages, page_size,
-          _at(out, "out", None, shape, dev), _dtype_code(out.dtype), _at(lse, "lse", torch.float32, (B, Hq), dev),
-          _at(workspace, "workspace", None, None, dev), workspace.nbytes)
+        _need(q, "q", None, 3)
+        _need(k_cache, "k_cache", None, 4)
+        n = zmoe_paged_attention_workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], k_cache.shape[3])
+        workspace = _out((max(n, 16),), torch.uint8, q.get_device(), stream, shared=False)
+    status = (_binding or _calls()).paged_attention(q, k_cache, v_cache, page_table, lens, scale, k_scale, v_scale, gate,
+                                                    out, lse, workspace, stream)
+    if status:
+        _check(status, "zmoe_paged_attention")
     return out
 
 
@@ -773,24 +697,14 @@ def zmoe_adjust_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = N
 
     repetition, presence, frequency: f32 [T]; ``out`` may be ``logits``.  ids: the lowest id of the largest
     adjusted logit, -1 when the mask leaves none."""
-    _need(logits, "logits", None, 3)
-    T, N, V = shape = logits.shape
-    dev = logits.get_device()
-    _on_device(stream, dev)
-    L = 0
-    if history is not None:
-        _need(history, "history", torch.int32, 3)
-        L = history.shape[1]
     if out is None:
-        out = _out(shape, logits.dtype, dev, stream)
+        out = _empty_for(logits, "logits", logits.shape, logits.dtype, stream)
     if ids is None:
-        ids = _out((T, N), torch.int32, dev, stream)
-    _call("zmoe_adjust_logits", dev, stream, logits.data_ptr(), _dtype_code(logits.dtype),
-          _at(history, "history", torch.int32, (T, L, N), dev), _at(hist_lens, "hist_lens", torch.int32, (T,), dev),
-          _at(repetition, "repetition", torch.float32, (T,), dev), _at(presence, "presence", torch.float32, (T,), dev),
-          _at(frequency, "frequency", torch.float32, (T,), dev), _at(bias, "bias", torch.float32, (N, V), dev),
-          _at(mask, "mask", torch.int32, (T, N, (V + 31) // 32), dev), T, N, V, L,
-          _at(out, "out", logits.dtype, shape, dev), _at(ids, "ids", torch.int32, (T, N), dev))
+        ids = _empty_for(logits, "logits", logits.shape[:2], torch.int32, stream)
+    status = (_binding or _calls()).adjust_logits(logits, history, hist_lens, repetition, presence, frequency, bias, mask,
+                                                  out, ids, stream)
+    if status:
+        _check(status, "zmoe_adjust_logits")
     return out, ids
 
 

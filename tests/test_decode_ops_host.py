@@ -196,3 +196,23 @@ def _cpu(*shape, dtype=torch.float32):
 def test_host_tensors_are_rejected(call):
     with pytest.raises(TypeError, match="must be a CUDA tensor"):
         call()
+
+
+def test_compiled_calls_refuse_what_is_no_tensor_and_wrong_counts():
+    b, t = Z._calls(), _cpu(2, 4)
+    for call, n in ((b.add_rmsnorm, 11), (b.kv_append, 17), (b.paged_attention, 13), (b.adjust_logits, 11)):
+        for args in ((t,) * n, (None,) * n, (1,) * n, ("x",) * n):
+            with pytest.raises(TypeError, match="must be a CUDA tensor"):
+                call(*args)
+        for args in ((), (t,) * (n - 1), (t,) * (n + 1)):
+            with pytest.raises(TypeError, match=f"{n} arguments wanted, got {len(args)}"):
+                call(*args)
+
+
+def test_missing_compiled_calls_fail_loudly(monkeypatch):
+    import sys
+    monkeypatch.setattr(Z, "_binding", None)
+    monkeypatch.setitem(sys.modules, "sparse_moe_decoder_b200._binding", None)
+    monkeypatch.delattr(sys.modules["sparse_moe_decoder_b200"], "_binding", raising=False)
+    with pytest.raises(ImportError, match="build it with"):
+        Z._calls()
