@@ -23,9 +23,9 @@ namespace zmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;      // tokens of one block
+constexpr int kMaxTokens = 8;      // tokens of one block
 constexpr int kMaxHalf = 64;       // pairs of one head (D <= 128)
-constexpr int kAhead = 2;          // heads in flight a group of lanes
+constexpr int kAhead = 1;          // heads in flight a group of lanes
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -68,7 +68,7 @@ __device__ __forceinline__ void store4(uint16_t* p, const float* v) {
 }
 
 template <typename TI, int D, bool FP8>
-__global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 16;                 // lanes of a head
   constexpr int kGroups = kThreads / kLanes;     // heads at a time
   __shared__ __align__(16) float cosine[kMaxTokens][kMaxHalf], sine[kMaxTokens][kMaxHalf];
@@ -311,7 +311,9 @@ extern "C" zmoe_status zmoe_kv_append(const void* q, const void* k, const void* 
   a.q_gamma = q_gamma; a.k_gamma = k_gamma; a.eps = eps;
   a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.n_seqs = n_seqs; a.n_pages = n_pages; a.page_size = page_size;
   a.max_pages = max_pages;
-  a.tokens = T > 4 * num_sms() ? kMaxTokens : 1;
+  // tokens of a block: up to 8, as long as there are two blocks for each SM
+  a.tokens = T / (2 * num_sms());
+  a.tokens = a.tokens < 1 ? 1 : (a.tokens < kMaxTokens ? a.tokens : kMaxTokens);
   a.q_out = static_cast<uint16_t*>(q_out);
   a.k_cache = k_cache; a.v_cache = v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
   a.page_table = page_table;

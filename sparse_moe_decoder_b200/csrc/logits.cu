@@ -9,7 +9,7 @@
 //
 // Bound by HBM for large vocabularies (logits read once, written once), by latency for one frame.  A row
 // (stream, codebook) is split over a cluster of 1 to 8 CTAs.  Each counts its ids' occurrences in shared memory
-// (16-bit counters, so up to 28672 ids a pass), passes over its logits once, and leaves its best (value, id) in
+// (16-bit counters, so up to 28160 ids a pass), passes over its logits once, and leaves its best (value, id) in
 // the first CTA's shared memory, which takes the largest: no workspace, one launch, and the order in which CTAs
 // finish does not matter.
 //
@@ -33,13 +33,21 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 2;          // vectors in flight a thread
-constexpr int kBlocks = 3;         // CTAs an SM
+#ifndef KA
+#define KA 2
+#endif
+#ifndef KB
+#define KB 3
+#endif
+constexpr int kAhead = KA;          // vectors in flight a thread
+constexpr int kBlocks = KB;         // CTAs an SM, of 256 threads
 constexpr int kMaxSplit = 8;       // the portable cluster size
-constexpr int kChunk = 28672;      // ids counted at a time
+constexpr int kChunk = 28160;      // ids counted at a time
 constexpr int kEnds = 32;          // ids at a row's two ends, at most 4 + 7 and 4 + 2 * 7
+constexpr int kEndVecs = 8;         // their vectors, rounded up
+constexpr int kMaxIds = kChunk + 8 * kEndVecs;
+constexpr int kMaxSmem = kMaxIds * 2 + kMaxIds / 8 + 4 + (kMaxIds + kEnds) * 6;   // counters, their bits, the list
+static_assert(kMaxSmem <= 226 * 1024, "one CTA an SM at least");
 constexpr int kMaxHistory = 65535; // what a 16-bit counter holds
 
 struct AdjustArgs {
@@ -52,7 +60,7 @@ struct AdjustArgs {
   const uint32_t* mask;       // [T, N, ceil(V / 32)] or null
   int32_t* ids;               // [T, N] or null
   int N, V, L, split;
-  int at_once;                // vectors counted at a time
+  int at_once;                // vectors counted at a time, beside those of the ends
   int list;                   // ids that can be listed, even
   int same;                   // logits and out lie alike within a vector
   unsigned int* errors;
@@ -143,15 +151,17 @@ struct Row {
   }
 };
 
-template <typename TL>
-__global__ void __launch_bounds__(kThreads, kBlocks) adjust_kernel(AdjustArgs a) {
+template <typename TL, int kThreads>
+__global__ void __launch_bounds__(kThreads, kBlocks * 256 / kThreads) adjust_kernel(AdjustArgs a) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint32_t counts[];   // 16-bit counters, one an id; behind them the list
   __shared__ int listed;
   __shared__ float best_v[kWarps];
   __shared__ uint32_t best_i[kWarps];
   __shared__ unsigned long long part[kMaxSplit];
-  // listed ids, as counters, and their logits
-  uint16_t* list_at = reinterpret_cast<uint16_t*>(counts + (a.history ? kE<TL> / 2 * a.at_once : 0));
+  // a bit for each counter that is not zero; listed ids, as counters, and their logits
+  uint32_t* seen = counts + kE<TL> / 2 * (a.at_once + kEndVecs);
+  uint16_t* list_at = reinterpret_cast<uint16_t*>(a.history ? seen + ((a.at_once + kEndVecs) * kE<TL> + 31) / 32 : counts);
   float* list_x = reinterpret_cast<float*>(list_at + a.list);
   const int rank = blockIdx.x % a.split, row = blockIdx.x / a.split;   // row = t * N + n
   const int t = row / a.N, n = row - t * a.N;
@@ -175,6 +185,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adjust_kernel(AdjustArgs a)
   const int low_end = E * i_low - shift < a.V ? E * i_low - shift : a.V;
   const int high_begin = E * i_high - shift > low_end ? E * i_high - shift : low_end;
   const int i_first = i_begin > i_low ? i_begin : i_low, i_last = i_end < i_high ? i_end : i_high;
+  // all of the row's share goes to the L2 cache while the ids are counted
+  if (threadIdx.x == 0 && i_first < i_last && i_last - i_first > kAhead * kThreads)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(r.src + (E * i_first - shift)),
+                 "r"((i_last - i_first) * 16));
   // all that the first counts and vectors need is asked for at once
   int32_t early[2];
 #pragma unroll
@@ -194,23 +208,25 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adjust_kernel(AdjustArgs a)
   uint32_t bi = 0xFFFFFFFFu;   // its id
   auto pass = [&](auto turn_c) {
     constexpr int TURN = decltype(turn_c)::value;
+    // This thread's vectors are kThreads apart from i_first on; its next kAhead are on their way at any time.
+    constexpr int kStep = kAhead * kThreads;
     Some<TL> f[kAhead];
-    auto fetch = [&](int at) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = at + static_cast<int>(threadIdx.x) + u * kThreads;
-        if (i < i_last) r.template load<TURN>(E * i - shift, f[u]);
-      }
-    };
-    fetch(i_first);
-    for (int c0 = i_begin; c0 < i_end; c0 += a.at_once) {
-      const int c1 = i_end - c0 < a.at_once ? i_end : c0 + a.at_once;
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i_first + static_cast<int>(threadIdx.x) + u * kThreads;
+      if (i < i_last) r.template load<TURN>(E * i - shift, f[u]);
+    }
+    // a chunk: `at_once` vectors (a multiple of kStep), and the ends of the row with the first and the last
+    for (int s0 = i_first; s0 == i_first ? i_begin < i_end : s0 < i_last; s0 += a.at_once) {
+      const int s1 = i_last - s0 < a.at_once ? i_last : s0 + a.at_once;
+      const int c0 = s0 == i_first ? i_begin : s0, c1 = s1 >= i_last ? i_end : s1;
       const int first = E * c0 - shift;   // the id of counter 0
       const unsigned span = static_cast<unsigned>(E * (c1 - c0));
       __syncthreads();   // the previous chunk's counts and list are read
       if (counted) {
         for (int i = threadIdx.x; i < (c1 - c0) * E / 4; i += kThreads)
           reinterpret_cast<uint2*>(counts)[i] = make_uint2(0u, 0u);
+        for (int i = threadIdx.x; i < ((c1 - c0) * E + 31) / 32; i += kThreads) seen[i] = 0u;
       }
       if (threadIdx.x == 0) listed = 0;
       __syncthreads();
@@ -224,8 +240,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adjust_kernel(AdjustArgs a)
           const unsigned at = static_cast<unsigned>(id - first);
           if (id >= 0 && at < span && id < a.V) {
             const uint32_t was = atomicAdd(&counts[at >> 1], 1u << ((at & 1) * 16));
-            if (((was >> ((at & 1) * 16)) & 0xFFFFu) == 0 && id >= low_end && id < high_begin)
+            if (((was >> ((at & 1) * 16)) & 0xFFFFu) == 0 && id >= low_end && id < high_begin) {
+              atomicOr(&seen[at >> 5], 1u << (at & 31));
               list_at[atomicAdd(&listed, 1)] = static_cast<uint16_t>(at);
+            }
           }
           if (id >= a.V && rank == 0 && c0 == 0) record_device_error(a.errors);   // a negative id is no id
         };
@@ -249,30 +267,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adjust_kernel(AdjustArgs a)
       for (int i = threadIdx.x; i < n_listed; i += kThreads) list_x[i] = as_float(r.src[first + list_at[i]]);
       if (static_cast<int>(threadIdx.x) < n_listed) ask(threadIdx.x);
       if (n_listed) __syncthreads();
-      const int s0 = c0 > i_first ? c0 : i_first, s1 = c1 < i_last ? c1 : i_last;
       int best_at = -1, allowed_at = -1;   // the vector of this chunk's best, and the first that allows an id
       Vec<TL> best;
       auto rest_of = [&](int i) -> uint32_t {   // bits of the vector's ids that are not listed
-        uint32_t c[E / 2], any = 0, rest = (1u << E) - 1;
-        if (E == 8) {
-          const uint4 q = reinterpret_cast<const uint4*>(counts)[i - c0];
-          c[0] = q.x; c[1] = q.y; c[E / 2 - 2] = q.z; c[E / 2 - 1] = q.w;
-        } else {
-          const uint2 q = reinterpret_cast<const uint2*>(counts)[i - c0];
-          c[0] = q.x; c[1] = q.y;
-        }
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k) any |= c[k];
-        if (any) {
-#pragma unroll
-          for (int k = 0; k < E / 2; ++k) {
-            if (c[k] & 0xFFFFu) rest &= ~(1u << (2 * k));
-            if (c[k] >> 16) rest &= ~(2u << (2 * k));
-          }
-        }
-        return rest;
+        return ~(seen[(i - c0) * E >> 5] >> ((i - c0) * E & 31)) & ((1u << E) - 1);
       };
-      for (int at = s0; at < s1; at += kAhead * kThreads) {
+      for (int at = s0; at < s1; at += kStep) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const int i = at + static_cast<int>(threadIdx.x) + u * kThreads, v = E * i - shift;
@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adjust_kernel(AdjustArgs a)
             best = o;
           }
           if (allowed_at < 0 && ok) allowed_at = i;
+          if (i + kStep < i_last) r.template load<TURN>(v + E * kStep, f[u]);   // of the next chunk too
         }
-        fetch(at + kAhead * kThreads < s1 ? at + kAhead * kThreads : s1);   // of the next chunk too
       }
       if (best_at >= 0) {
         float x[E];
@@ -391,10 +391,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adjust_kernel(AdjustArgs a)
   }
 }
 
-template <typename TL>
+template <typename TL, int kThreads>
 zmoe_status launch(const AdjustArgs& a, int rows, size_t smem, cudaStream_t s) {
-  if (smem > 40 * 1024 && cudaFuncSetAttribute(adjust_kernel<TL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kChunk * 8 + kEnds * 6) != cudaSuccess)
+  if (smem > 40 * 1024 && cudaFuncSetAttribute(adjust_kernel<TL, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMaxSmem) != cudaSuccess)
     return check_launch("zmoe_adjust_logits: shared memory attribute");
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(rows) * a.split);
@@ -407,8 +407,8 @@ zmoe_status launch(const AdjustArgs& a, int rows, size_t smem, cudaStream_t s) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, adjust_kernel<TL>, a);
+  cfg.numAttrs = a.split > 1 ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, adjust_kernel<TL, kThreads>, a);
   return check_launch("zmoe_adjust_logits");
 }
 
@@ -455,12 +455,16 @@ extern "C" zmoe_status zmoe_adjust_logits(const void* logits, zmoe_dtype dtype, 
   a.split = split;
   const int E = dtype == ZMOE_BF16 ? 8 : 4;
   const int vecs = ((V + 2 * E - 2) / E + split - 1) / split;
-  const int chunks = (vecs + kChunk / E - 1) / (kChunk / E);
-  a.at_once = (vecs + chunks - 1) / chunks;
+  const int threads = vecs <= 2 * kAhead * 128 ? 128 : 256;   // short rows: smaller CTAs, so that more rows run at once
+  const int step = kAhead * threads, most = kChunk / E / step * step, chunks = (vecs + most - 1) / most;
+  a.at_once = ((vecs + chunks - 1) / chunks + step - 1) / step * step;
+  const int counters = E * (a.at_once + kEndVecs);
   a.list = kEnds;
-  if (a.history) a.list += ((L < E * a.at_once ? L : E * a.at_once) + 1) & ~1;
-  const size_t smem = (a.history ? static_cast<size_t>(a.at_once) * E * 2 : 0) + static_cast<size_t>(a.list) * 6;
+  if (a.history) a.list += ((L < counters ? L : counters) + 1) & ~1;
+  const size_t smem = (a.history ? static_cast<size_t>(counters) * 2 + (counters + 31) / 32 * 4 : 0) + static_cast<size_t>(a.list) * 6;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return dtype == ZMOE_BF16 ? launch<uint16_t>(a, static_cast<int>(rows), smem, s)
-                            : launch<float>(a, static_cast<int>(rows), smem, s);
+  const int n = static_cast<int>(rows);
+  if (threads == 128)
+    return dtype == ZMOE_BF16 ? launch<uint16_t, 128>(a, n, smem, s) : launch<float, 128>(a, n, smem, s);
+  return dtype == ZMOE_BF16 ? launch<uint16_t, 256>(a, n, smem, s) : launch<float, 256>(a, n, smem, s);
 }
