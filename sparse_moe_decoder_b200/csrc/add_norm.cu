@@ -17,6 +17,7 @@
 namespace zmoe {
 namespace {
 
+constexpr char kName[] = "zmoe_add_rmsnorm";
 constexpr int kRowThreads = 512;   // threads a row is spread over at most
 constexpr int kMaxD = 32768;       // 512 threads with 64 columns each
 
@@ -44,12 +45,13 @@ __global__ void __launch_bounds__(kRowThreads) add_rmsnorm_kernel(AddNormArgs a)
   constexpr int kVecs = CH / 8;      // vectors of 8 columns a chunk
   constexpr bool kKeep = CH == 16 && N == 1;   // the gains stay in registers from row to row
   __shared__ float red[2][2][kRowThreads / 32];   // [row parity][sum, largest]
+  enter_behind();
   const int warps_row = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = threadIdx.x * CH, step = blockDim.x * CH;
   float kept[kKeep ? kVecs : 1][8];
   auto gains = [&](int c, float* g) {
-    const float4 g0 = __ldg(reinterpret_cast<const float4*>(a.gamma + c));
-    const float4 g1 = __ldg(reinterpret_cast<const float4*>(a.gamma + c) + 1);
+    const float4 g0 = *(reinterpret_cast<const float4*>(a.gamma + c));
+    const float4 g1 = *(reinterpret_cast<const float4*>(a.gamma + c) + 1);
     g[0] = g0.x; g[1] = g0.y; g[2] = g0.z; g[3] = g0.w;
     g[4] = g1.x; g[5] = g1.y; g[6] = g1.z; g[7] = g1.w;
   };
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kRowThreads) add_rmsnorm_kernel(AddNormArgs a)
 
 // Chunks a thread holds: one as long as 256 threads reach a row's end.
 template <typename TH, typename TD, typename TX, int CH>
-void launch_row(const AddNormArgs& a, cudaStream_t s) {
+zmoe_status launch_row(const AddNormArgs& a, cudaStream_t s) {
   const int chunks = (a.d + CH - 1) / CH;
   int n = 1;
   while (chunks > 256 * n && n * CH < 64) n *= 2;
@@ -206,18 +208,17 @@ void launch_row(const AddNormArgs& a, cudaStream_t s) {
     grid = (grid + (grid + most - 1) / most - 1) / ((grid + most - 1) / most);
   }
   switch (n) {
-    case 1: add_rmsnorm_kernel<TH, TD, TX, CH, 1><<<grid, block, 0, s>>>(a); break;
-    case 2: add_rmsnorm_kernel<TH, TD, TX, CH, 2><<<grid, block, 0, s>>>(a); break;
-    case 4: add_rmsnorm_kernel<TH, TD, TX, CH, 4><<<grid, block, 0, s>>>(a); break;
-    default: add_rmsnorm_kernel<TH, TD, TX, CH, 64 / CH><<<grid, block, 0, s>>>(a); break;
+    case 1: return launch_behind(kName, add_rmsnorm_kernel<TH, TD, TX, CH, 1>, dim3(grid), block, 0, s, 1, a);
+    case 2: return launch_behind(kName, add_rmsnorm_kernel<TH, TD, TX, CH, 2>, dim3(grid), block, 0, s, 1, a);
+    case 4: return launch_behind(kName, add_rmsnorm_kernel<TH, TD, TX, CH, 4>, dim3(grid), block, 0, s, 1, a);
+    default: return launch_behind(kName, add_rmsnorm_kernel<TH, TD, TX, CH, 64 / CH>, dim3(grid), block, 0, s, 1, a);
   }
 }
 
 template <typename TH, typename TD>
-void launch_x(const AddNormArgs& a, zmoe_dtype xt, cudaStream_t s) {
+zmoe_status launch_x(const AddNormArgs& a, zmoe_dtype xt, cudaStream_t s) {
   constexpr int CH = sizeof(TH) + sizeof(TD) == 4 ? 16 : 8;
-  if (xt == ZMOE_BF16) launch_row<TH, TD, uint16_t, CH>(a, s);
-  else launch_row<TH, TD, float, CH>(a, s);
+  return xt == ZMOE_BF16 ? launch_row<TH, TD, uint16_t, CH>(a, s) : launch_row<TH, TD, float, CH>(a, s);
 }
 
 }  // namespace
@@ -247,12 +248,7 @@ extern "C" zmoe_status zmoe_add_rmsnorm(const void* h, zmoe_dtype h_dtype, const
   clear_error();
   const AddNormArgs a{h, delta, gamma, eps, 1.f / static_cast<float>(d), T, d, group, h_out, x, codes, scales};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (h_dtype == ZMOE_BF16) {
-    if (delta_dtype == ZMOE_BF16) launch_x<uint16_t, uint16_t>(a, x_dtype, s);
-    else launch_x<uint16_t, float>(a, x_dtype, s);
-  } else {
-    if (delta_dtype == ZMOE_BF16) launch_x<float, uint16_t>(a, x_dtype, s);
-    else launch_x<float, float>(a, x_dtype, s);
-  }
-  return check_launch("zmoe_add_rmsnorm");
+  if (h_dtype == ZMOE_BF16)
+    return delta_dtype == ZMOE_BF16 ? launch_x<uint16_t, uint16_t>(a, x_dtype, s) : launch_x<uint16_t, float>(a, x_dtype, s);
+  return delta_dtype == ZMOE_BF16 ? launch_x<float, uint16_t>(a, x_dtype, s) : launch_x<float, float>(a, x_dtype, s);
 }

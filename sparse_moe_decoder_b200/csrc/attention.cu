@@ -5,10 +5,10 @@
 //   s_t = scale q_i . k_t;   o_i = sum_t exp(s_t) v_t / sum_t exp(s_t),  t < n;   lse_i = log sum_t exp(s_t)
 //   out_i = sigmoid(gate_i) o_i                                               (o = 0, lse = -inf when n = 0)
 //
-// Bound by HBM: every cached key and value is read once (per 8 or 16 query heads of a group).  A warp takes 16
-// tokens at a time, which lie in one page.  Their keys, then their values, come by TMA into the warp's own ring in
-// shared memory (128-byte swizzle, an mbarrier a slot), 12 to 24 KB ahead of the products; 16 warps an SM keep
-// 192 KB in flight, and no warp waits for another.
+// Bound by HBM: every cached key and value is read once (per 8 or 16 query heads of a group).  A warp takes 8 KB of
+// them at a time, a step of 16 (bf16, 128 columns) to 64 tokens; each 16 of these lie in one page, and their keys
+// and their values come by one TMA copy each into the warp's own ring in shared memory (128-byte swizzle, an mbarrier
+// a step, two steps), so 12 warps keep up to 192 KB an SM in flight, and no warp waits for another.
 //   scores  S = Q K^T:      m16n8k16, 16 rows of query heads (8 or 16 in use), 8 tokens, 16 columns;
 //   output  O^T = V^T P^T:  m16n8k16, 16 columns of V, 8 query heads, 16 tokens.
 // (A tcgen05 product has at least 64 rows, of which a group's heads would fill 4 or 8, and its accumulator lies in
@@ -44,7 +44,7 @@ using namespace ptx;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kJoinThreads = 256;
-constexpr int kMaxWarpsPerSm = 16;
+constexpr int kMaxWarpsPerSm = 12;
 constexpr uint64_t kWaitNs = 2000000000ull;   // a wait for a copy gives up after this
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -99,9 +99,11 @@ __device__ __forceinline__ float pow2(float x) {
   return y;
 }
 
-// Tiles of 16 tokens of sequence b; a length beyond the table's pages is an error and cut to them.
+// The length of sequence b; one beyond the table's pages is an error and cut to them.  EARLY: read past the L1 cache,
+// by a kernel that has not waited for the one before it yet.
+template <bool EARLY = false>
 __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
-  const int n = __ldg(a.lens + b);
+  const int n = EARLY ? __ldcg(a.lens + b) : a.lens[b];
   const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
   return n < 0 ? 0 : (n > cap ? static_cast<int>(cap) : n);
 }
@@ -224,7 +226,7 @@ __device__ __forceinline__ void store2<uint16_t>(uint16_t* p, float x, float y) 
 }
 
 __device__ __forceinline__ float gate_of(const AttnArgs& a, int b, int head) {
-  return a.gate ? 1.f / (1.f + expf(-__ldg(a.gate + static_cast<size_t>(b) * a.Hq + head))) : 1.f;
+  return a.gate ? 1.f / (1.f + expf(-*(a.gate + static_cast<size_t>(b) * a.Hq + head))) : 1.f;
 }
 
 template <int D, bool FP8, int HT, typename TO>
@@ -239,7 +241,6 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
   __shared__ long long scan[kWarps];
   __shared__ int at_b[kWarps];
   __shared__ long long at_off[kWarps];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
   const int units = a.Hkv * a.gtiles;
   uint64_t* bar = bars[warp];
@@ -250,13 +251,15 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
     for (int i = 0; i < L::slots; ++i) mbar_init(bar + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
   }
+  // what came before is complete, and only now may the second kernel begin: it reads the lengths before its own wait
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
   // the line of tiles: sequence by sequence, in each the groups, in each the tiles
   const int per = (a.B + kThreads - 1) / kThreads, b_lo = threadIdx.x * per;
   const int b_hi = b_lo + per < a.B ? b_lo + per : a.B;
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     mine += static_cast<long long>(tiles_of(seq_len(a, b))) * units;
-    if (blockIdx.x == 0 && __ldg(a.lens + b) > static_cast<long long>(a.max_pages) * a.page_size)
+    if (blockIdx.x == 0 && a.lens[b] > static_cast<long long>(a.max_pages) * a.page_size)
       record_device_error(a.errors);
   }
   long long total;
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
     int line = -1;
     if (t < f_nt && t - f_tile < f_left) {
       const int col = t / tpp;
-      const int pid = __ldg(a.table + static_cast<size_t>(f_b) * a.max_pages + col);
+      const int pid = *(a.table + static_cast<size_t>(f_b) * a.max_pages + col);
       if (pid >= 0 && pid < a.n_pages)
         line = ((pid * a.Hkv + f_u / a.gtiles) * a.page_size + (t - col * tpp) * 16) >> (L::row == 64 ? 1 : 0);
       else if (f_u == 0 && (t == f_tile || t == col * tpp))
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
       for (int c = 0; c < D / 32; ++c) {
         // the columns of lane j's key chunks: 8 a chunk (bf16), 16 (8-bit cache)
         const int col = FP8 ? L::k_chunk(c >> 1, j) * 16 + (c & 1) * 8 : L::k_chunk(c, j) * 8;
-        raw[c] = on ? __ldg(reinterpret_cast<const uint4*>(qr + col)) : make_uint4(0u, 0u, 0u, 0u);
+        raw[c] = on ? *(reinterpret_cast<const uint4*>(qr + col)) : make_uint4(0u, 0u, 0u, 0u);
       }
       if (r < HT) qs[r] = a.scale * kLog2e;
       if (FP8) {
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
         // the largest magnitude goes to [2^14, 2^15), unless it is below 2^-86: such a query scores 0 anyway
         const int bits = static_cast<int>(__float_as_uint(top) >> 23), ex = bits == 255 ? 0 : (bits < 41 ? 100 : 141 - bits);
         const float up = __int_as_float((127 + ex) << 23);
-        if (r < HT) qs[r] = a.scale * kLog2e * __ldg(a.k_scale + hk) * __int_as_float((127 - ex) << 23);
+        if (r < HT) qs[r] = a.scale * kLog2e * a.k_scale[hk] * __int_as_float((127 - ex) << 23);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float f[8];
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
     const bool whole = tile == 0 && t_end == nt;
     const int part_slot = todo == piece ? 0 : 1;
     float* part = a.parts + (static_cast<size_t>(gw) * 2 + part_slot) * part_floats<D, HT>();
-    const float vs = FP8 ? __ldg(a.v_scale + hk) / kPScale : 1.f;
+    const float vs = FP8 ? a.v_scale[hk] / kPScale : 1.f;
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -677,16 +680,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
   const int per = (a.B + kJoinThreads - 1) / kJoinThreads, b_lo = threadIdx.x * per;
   const int b_hi = b_lo + per < a.B ? b_lo + per : a.B;
   long long mine = 0;
-  for (int i = b_lo; i < b_hi; ++i) mine += static_cast<long long>(tiles_of(seq_len(a, i))) * units;
+  for (int i = b_lo; i < b_hi; ++i) mine += static_cast<long long>(tiles_of(seq_len<true>(a, i))) * units;
   long long total;
   const long long pre = block_prefix<kJoinWarps>(mine, scan, total);
   if (b >= b_lo && b < b_hi) {
     long long p = pre;
-    for (int i = b_lo; i < b; ++i) p += static_cast<long long>(tiles_of(seq_len(a, i))) * units;
+    for (int i = b_lo; i < b; ++i) p += static_cast<long long>(tiles_of(seq_len<true>(a, i))) * units;
     start_of_b = p;
   }
   __syncthreads();
-  const int nt = tiles_of(seq_len(a, b));
+  const int nt = tiles_of(seq_len<true>(a, b));
   TO* out = static_cast<TO*>(a.out) + (static_cast<size_t>(b) * a.Hq + hq) * D;
   if (nt == 0) {   // the first kernel does not touch these rows, and it began behind what came before both
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -697,14 +700,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
     }
     return;
   }
-  const long long p0 = start_of_b + static_cast<long long>(hk * a.gtiles + gt) * nt, p1 = p0 + nt;
+  const long long p0 = start_of_b + static_cast<long long>(hk * a.gtiles + gt) * nt;
   const Pieces pieces(total, a.warps);
-  const int w0 = pieces.owner(p0), parts = pieces.owner(p1 - 1) - w0 + 1;
+  const int w0 = pieces.owner(p0), parts = pieces.owner(p0 + nt - 1) - w0 + 1;
   if (parts == 1) return;   // written whole
   const float* base = a.parts + static_cast<size_t>(w0) * 2 * part_floats<D, HT>();
   const int first_slot = pieces.start(w0) == p0 ? 0 : 1;
   auto part_of = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? first_slot : 0)) * part_floats<D, HT>(); };
-  // every thread of the first kernel's grid is done, and its writes are visible, behind this line
+  // The first kernel's grid is done, and its writes are visible, behind this line.  What comes next is not let in
+  // early: the blocks of the next step's first kernel fill the machine, and came to lie unevenly beside these (64 to
+  // 77 us a call at 286k E4M3 tokens).
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kBatch = 8;   // parts in flight, with a running maximum
   float m = __int_as_float(0xff800000), l = 0.f;
@@ -787,25 +792,17 @@ zmoe_status launch(AttnArgs a, cudaStream_t s) {
     return fail(ZMOE_ERR_CUDA, "zmoe_paged_attention: the cache's tensor map cannot be made");
   if (cudaFuncSetAttribute(attn_kernel<D, FP8, HT, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem) != cudaSuccess)
     return check_launch("zmoe_paged_attention: shared memory attribute");
-  attn_kernel<D, FP8, HT, TO><<<blocks, kThreads, L::smem, s>>>(km, vm, a);
-  zmoe_status st = check_launch("zmoe_paged_attention");
+  const zmoe_status st = launch_behind("zmoe_paged_attention", attn_kernel<D, FP8, HT, TO>, dim3(blocks), dim3(kThreads),
+                                       L::smem, s, 1, km, vm, a);
   if (st != ZMOE_OK) return st;
-  cudaLaunchConfig_t cfg{};
   // A block a head, unless they are more than run at once: then it takes up to 8 heads of a group.
   a.together = 1;
   while (static_cast<long long>(a.B) * a.Hkv * ((a.G + a.together - 1) / a.together) > 3LL * num_sms() &&
          a.together < 8 && a.together < a.G)
     a.together *= 2;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.Hkv * ((a.G + a.together - 1) / a.together));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, join_kernel<D, HT, TO>, a);
-  return check_launch("zmoe_paged_attention (join)");
+  return launch_behind("zmoe_paged_attention (join)", join_kernel<D, HT, TO>,
+                       dim3(static_cast<unsigned>(a.B) * a.Hkv * ((a.G + a.together - 1) / a.together)),
+                       dim3(kJoinThreads), 0, s, 1, a);
 }
 
 template <int D, bool FP8>

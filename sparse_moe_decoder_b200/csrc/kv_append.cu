@@ -50,13 +50,13 @@ struct Raw4;
 template <>
 struct Raw4<float> {
   float4 r;
-  __device__ __forceinline__ void load(const float* p) { r = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void load(const float* p) { r = *(reinterpret_cast<const float4*>(p)); }
   __device__ __forceinline__ void get(float* v) const { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
 };
 template <>
 struct Raw4<uint16_t> {
   uint2 r;
-  __device__ __forceinline__ void load(const uint16_t* p) { r = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void load(const uint16_t* p) { r = *(reinterpret_cast<const uint2*>(p)); }
   __device__ __forceinline__ void get(float* v) const {
     widen_bf16x2(r.x, v);
     widen_bf16x2(r.y, v + 2);
@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(AppendArgs a) {
   constexpr int kGroups = kThreads / kLanes;     // heads at a time
   __shared__ __align__(16) float cosine[kMaxTokens][kMaxHalf], sine[kMaxTokens][kMaxHalf];
   __shared__ long long slot[kMaxTokens];         // cache row of head 0: page * Hkv * page_size + row; -1: skip
+  enter_behind();
   const int t0 = blockIdx.x * a.tokens;
   const int nt = a.T - t0 < a.tokens ? a.T - t0 : a.tokens;
   const int half = a.rot >> 1;
@@ -136,12 +137,12 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(AppendArgs a) {
   fetch();
   if (threadIdx.x < nt) {
     const int t = t0 + threadIdx.x;
-    const int s = a.seq ? __ldg(a.seq + t) : t, p = __ldg(a.pos + t);
+    const int s = a.seq ? a.seq[t] : t, p = a.pos[t];
     long long to = -1;
     if (s >= 0) {   // a negative sequence marks a padding token
       const bool ok = s < a.n_seqs && p >= 0 && p < static_cast<long long>(a.max_pages) * a.page_size;
       const int col = ok ? static_cast<int>(static_cast<unsigned>(p) / static_cast<unsigned>(a.page_size)) : 0;
-      const int page = ok ? __ldg(a.page_table + static_cast<size_t>(s) * a.max_pages + col) : -1;
+      const int page = ok ? *(a.page_table + static_cast<size_t>(s) * a.max_pages + col) : -1;
       if (page >= 0 && page < a.n_pages)
         to = static_cast<long long>(page) * a.Hkv * a.page_size + (p - col * a.page_size);
       else
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(AppendArgs a) {
     const int t = i / kMaxHalf, f = i % kMaxHalf;
     if (t < nt && f < half) {
       const double turns =
-          static_cast<double>(__ldg(a.pos + t0 + t)) * __ldg(a.inv_freq + f) * 0.15915494309189533577;   // 1 / (2 pi)
+          static_cast<double>(*(a.pos + t0 + t)) * a.inv_freq[f] * 0.15915494309189533577;   // 1 / (2 pi)
       float sn, cs;
       sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn, &cs);
       cosine[t][f] = cs;
@@ -180,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(AppendArgs a) {
           const float inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma + cols[k].c0));
-            const float4 g1 = __ldg(reinterpret_cast<const float4*>(gamma + cols[k].c1));
+            const float4 g0 = *(reinterpret_cast<const float4*>(gamma + cols[k].c0));
+            const float4 g1 = *(reinterpret_cast<const float4*>(gamma + cols[k].c1));
             const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[k][e] = x[k][e] * inv * g[e];
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(AppendArgs a) {
         const size_t row = static_cast<size_t>(to + static_cast<long long>(hh) * a.page_size) * D;
         void* cache = key ? a.k_cache : a.v_cache;
         if (FP8) {
-          const float rs = __frcp_rn(__ldg((key ? a.k_scale : a.v_scale) + hh));
+          const float rs = __frcp_rn(*((key ? a.k_scale : a.v_scale) + hh));
           uint8_t* dst = static_cast<uint8_t*>(cache) + row;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -249,15 +250,10 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(AppendArgs a) {
   }
 }
 
-template <typename TI>
-void launch(const AppendArgs& a, int D, bool fp8, int grid, cudaStream_t s) {
-  if (D == 64) {
-    if (fp8) kv_append_kernel<TI, 64, true><<<grid, kThreads, 0, s>>>(a);
-    else kv_append_kernel<TI, 64, false><<<grid, kThreads, 0, s>>>(a);
-  } else {
-    if (fp8) kv_append_kernel<TI, 128, true><<<grid, kThreads, 0, s>>>(a);
-    else kv_append_kernel<TI, 128, false><<<grid, kThreads, 0, s>>>(a);
-  }
+template <typename TI, int D>
+zmoe_status launch(const AppendArgs& a, bool fp8, int grid, cudaStream_t s) {
+  return launch_behind("zmoe_kv_append", fp8 ? kv_append_kernel<TI, D, true> : kv_append_kernel<TI, D, false>, dim3(grid),
+                       dim3(kThreads), 0, s, 1, a);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -320,7 +316,7 @@ extern "C" zmoe_status zmoe_kv_append(const void* q, const void* k, const void* 
   a.errors = device_error_counter();
   const int grid = (T + a.tokens - 1) / a.tokens;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (in_dtype == ZMOE_BF16) launch<uint16_t>(a, D, kv_dtype == ZMOE_E4M3, grid, s);
-  else launch<float>(a, D, kv_dtype == ZMOE_E4M3, grid, s);
-  return check_launch("zmoe_kv_append");
+  const bool fp8 = kv_dtype == ZMOE_E4M3;
+  if (in_dtype == ZMOE_BF16) return D == 64 ? launch<uint16_t, 64>(a, fp8, grid, s) : launch<uint16_t, 128>(a, fp8, grid, s);
+  return D == 64 ? launch<float, 64>(a, fp8, grid, s) : launch<float, 128>(a, fp8, grid, s);
 }

@@ -33,14 +33,8 @@ namespace {
 
 using namespace ptx;
 
-#ifndef KA
-#define KA 2
-#endif
-#ifndef KB
-#define KB 3
-#endif
-constexpr int kAhead = KA;          // vectors in flight a thread
-constexpr int kBlocks = KB;         // CTAs an SM, of 256 threads
+constexpr int kAhead = 2;           // vectors in flight a thread
+constexpr int kBlocks = 3;         // CTAs an SM, of 256 threads
 constexpr int kMaxSplit = 8;       // the portable cluster size
 constexpr int kChunk = 28160;      // ids counted at a time
 constexpr int kEnds = 32;          // ids at a row's two ends, at most 4 + 7 and 4 + 2 * 7
@@ -136,13 +130,13 @@ struct Row {
     constexpr int E = kE<TL>;
     f.x.load(src + v);
     f.ok = (1u << E) - 1;
-    if (mask) f.ok &= __funnelshift_r(__ldg(mask + (v >> 5)), __ldg(mask + ((v + E - 1) >> 5)), v & 31);
+    if (mask) f.ok &= __funnelshift_r(*(mask + (v >> 5)), *(mask + ((v + E - 1) >> 5)), v & 31);
     if (TURN >= 0) {
       const float4* p = reinterpret_cast<const float4*>(bias + v - TURN);
       float w[E + 4];
 #pragma unroll
       for (int i = 0; i < (TURN ? E / 4 + 1 : E / 4); ++i) {
-        const float4 q = __ldg(p + i);
+        const float4 q = p[i];
         w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
       }
 #pragma unroll
@@ -163,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks * 256 / kThreads) adjust_ker
   uint32_t* seen = counts + kE<TL> / 2 * (a.at_once + kEndVecs);
   uint16_t* list_at = reinterpret_cast<uint16_t*>(a.history ? seen + ((a.at_once + kEndVecs) * kE<TL> + 31) / 32 : counts);
   float* list_x = reinterpret_cast<float*>(list_at + a.list);
+  enter_behind();
   const int rank = blockIdx.x % a.split, row = blockIdx.x / a.split;   // row = t * N + n
   const int t = row / a.N, n = row - t * a.N;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -194,15 +189,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks * 256 / kThreads) adjust_ker
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = static_cast<int>(threadIdx.x) + u * kThreads;
-    early[u] = counted && i < a.L ? __ldg(hist + static_cast<size_t>(i) * a.N) : -1;
+    early[u] = counted && i < a.L ? *(hist + static_cast<size_t>(i) * a.N) : -1;
   }
   int len = 0;
   if (counted) {
-    len = a.hist_lens ? __ldg(a.hist_lens + t) : a.L;
+    len = a.hist_lens ? a.hist_lens[t] : a.L;
     len = len < 0 ? 0 : (len > a.L ? a.L : len);
   }
-  const float rep = a.repetition ? __ldg(a.repetition + t) : 1.f, pre = a.presence ? __ldg(a.presence + t) : 0.f,
-              frq = a.frequency ? __ldg(a.frequency + t) : 0.f;
+  const float rep = a.repetition ? a.repetition[t] : 1.f, pre = a.presence ? a.presence[t] : 0.f,
+              frq = a.frequency ? a.frequency[t] : 0.f;
   const float none = __int_as_float(0xff800000);
   float bv = none;             // the best of this thread so far
   uint32_t bi = 0xFFFFFFFFu;   // its id
@@ -251,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks * 256 / kThreads) adjust_ker
         for (int u = 0; u < 2; ++u)
           if (static_cast<int>(threadIdx.x) + u * kThreads < len) count(early[u]);
 #pragma unroll 4
-        for (int i = threadIdx.x + 2 * kThreads; i < len; i += kThreads) count(__ldg(hist + static_cast<size_t>(i) * a.N));
+        for (int i = threadIdx.x + 2 * kThreads; i < len; i += kThreads) count(*(hist + static_cast<size_t>(i) * a.N));
       }
       __syncthreads();
       // the listed logits are read before the pass writes anything, for `out` may be `logits`
@@ -260,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks * 256 / kThreads) adjust_ker
       bool lok = true;
       auto ask = [&](int i) {   // the bias and the mask of a listed id
         const int id = first + list_at[i];
-        if (TURN >= 0) lb = __ldg(r.bias + id);
-        if (r.mask) lok = (__ldg(r.mask + (id >> 5)) >> (id & 31)) & 1u;
+        if (TURN >= 0) lb = r.bias[id];
+        if (r.mask) lok = (*(r.mask + (id >> 5)) >> (id & 31)) & 1u;
       };
 #pragma unroll 2
       for (int i = threadIdx.x; i < n_listed; i += kThreads) list_x[i] = as_float(r.src[first + list_at[i]]);
@@ -396,20 +391,8 @@ zmoe_status launch(const AdjustArgs& a, int rows, size_t smem, cudaStream_t s) {
   if (smem > 40 * 1024 && cudaFuncSetAttribute(adjust_kernel<TL, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kMaxSmem) != cudaSuccess)
     return check_launch("zmoe_adjust_logits: shared memory attribute");
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows) * a.split);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.split > 1 ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, adjust_kernel<TL, kThreads>, a);
-  return check_launch("zmoe_adjust_logits");
+  return launch_behind("zmoe_adjust_logits", adjust_kernel<TL, kThreads>, dim3(static_cast<unsigned>(rows) * a.split),
+                       dim3(kThreads), smem, s, a.split, a);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
