@@ -1,8 +1,8 @@
 // The argument checks and calls of the decode-step operators for Python.
 //
 // A decode step makes these calls once a layer, and their kernels take a few microseconds at decode sizes; checking a
-// dozen tensors and converting thirty arguments in Python took two to three times as long as the launch (10 to 15 us
-// a call against 5 to 8 here).  Each function checks its tensors (type, shape, device, layout), raises TypeError or
+// dozen tensors and converting thirty arguments in Python took several times as long as the launch (10 to 15 us of
+// host time a call against 4 to 7 here).  Each function checks its tensors (type, shape, device, layout), raises TypeError or
 // ValueError, calls the C entry point on the tensors' device and on its current stream (or the one given), and
 // returns the entry point's status.
 #include <Python.h>
@@ -281,6 +281,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* gate = address(a[8], "gate", c.dev, {B, Hq}, at::kFloat);
     void* out = address(a[9], "out", c.dev, {B, Hq, c.D}, at::kFloat, true);
     void* lse = address(a[10], "lse", c.dev, {B, Hq}, at::kFloat);
+    const zmoe_dtype out_type = code_of(cuda_tensor(a[9], "out"));
     const at::Tensor& ws = contiguous(a[11], "workspace", -1);
     need_device(ws, "workspace", c.dev);
     const double scale = a[5] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.D)) : real(a[5], "scale");
@@ -289,7 +290,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 static_cast<const int32_t*>(lens), static_cast<const float*>(gate), static_cast<float>(scale),
                                 size32(B, "B"), size32(Hq, "Hq"), size32(c.Hkv, "Hkv"), size32(c.D, "D"), table.cols,
                                 size32(c.n_pages, "n_pages"), size32(c.page_size, "page_size"), out,
-                                code_of(THPVariable_Unpack(a[9])), static_cast<float*>(lse), ws.data_ptr(), ws.nbytes(),
+                                out_type, static_cast<float*>(lse), ws.data_ptr(), ws.nbytes(),
                                 at.stream);
   });
 }

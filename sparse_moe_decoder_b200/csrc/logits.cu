@@ -180,10 +180,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks * 256 / kThreads) adjust_ker
   const int low_end = E * i_low - shift < a.V ? E * i_low - shift : a.V;
   const int high_begin = E * i_high - shift > low_end ? E * i_high - shift : low_end;
   const int i_first = i_begin > i_low ? i_begin : i_low, i_last = i_end < i_high ? i_end : i_high;
-  // all of the row's share goes to the L2 cache while the ids are counted
-  if (threadIdx.x == 0 && i_first < i_last && i_last - i_first > kAhead * kThreads)
+  // the row's share (its first 256 KB: the CTAs' together fit the L2 cache) is on its way while the ids are counted
+  if (threadIdx.x == 0 && i_last - i_first > kAhead * kThreads)
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(r.src + (E * i_first - shift)),
-                 "r"((i_last - i_first) * 16));
+                 "r"((i_last - i_first < 16384 ? i_last - i_first : 16384) * 16));
   // all that the first counts and vectors need is asked for at once
   int32_t early[2];
 #pragma unroll

@@ -90,6 +90,15 @@ def test_norm_matches_the_formula(T, d, types):
     assert zmoe_get_device_errors() == 0
 
 
+def test_norm_several_rows_a_block():
+    """More 16-bit rows than blocks run at once: a block takes several, the last ones fewer."""
+    for T, d, group in ((3001, 2048, 128), (2999, 4096, 0), (5000, 264, 0)):
+        r = rnd(T)
+        h, delta = (dev(r.standard_normal((T, d)) * s, BF16) for s in (3, 1))
+        gamma = dev(1 + 0.2 * r.standard_normal(d), F32)
+        check_norm(zmoe_add_rmsnorm(h, gamma, delta, want_codes=True, group=group), h, delta, gamma, 1e-6, BF16, group)
+
+
 def test_norm_single_outputs_and_no_delta():
     r = rnd(5)
     h, gamma = dev(r.standard_normal((7, 384)), F32), dev(r.standard_normal(384), F32)
@@ -244,6 +253,11 @@ def test_append_many_tokens_and_an_odd_page():
                 48, 6)
 
 
+def test_append_blocks_of_eight_tokens():
+    n = 2501
+    append_case(13, [i % 5 for i in range(n)], [i // 5 for i in range(n)], 3, 1, 64, 32, True, True, "f32", "e4m3", 32, 16)
+
+
 def test_append_far_positions():
     append_case(4, [0, 1, 2], [1000003, 524288, 2 ** 21 - 1], 2, 1, 128, 128, True, False, "f32", "bf16", 16384, 128)
 
@@ -361,6 +375,27 @@ def test_attention_pages_and_tables(page):
 def test_attention_long_and_ragged():
     attn_case(1, [20011, 3, 0, 777, 16], 4, 1, 128, "bf16", 64, F32)
     attn_case(2, [30000, 1], 2, 1, 64, "e4m3", 32, F32, gate=True)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,D", [(12, 64), (16, 128)])
+def test_attention_wide_groups_over_long_caches(Hq, D, kv):
+    """16 heads at a time, more than one window of pages a piece, a group that ends inside a step."""
+    attn_case(Hq, [6007, 2, 1500], Hq, 1, D, kv, 48, F32, gate=True)
+    attn_case(Hq + 1, [70001], Hq, 1, D, kv, 16, BF16)
+
+
+def test_attention_sequences_that_share_pages():
+    r = rnd(15)
+    kc, vc, _, _ = make_cache(r, 9, 2, 16, 128, "bf16")
+    table = np.array([[3, 1, 4, 0], [3, 1, 5, 0], [3, 3, 3, 3]], np.int32)
+    lens = [60, 41, 64]
+    q = dev(r.standard_normal((3, 4, 128)), BF16)
+    out = f64(zmoe_paged_attention(q, kc, vc, dev(table), dev(np.array(lens, np.int32))))
+    for b, n in enumerate(lens):
+        want, _ = oracle.attend(f64(q[b]), oracle.paged_rows(f64(kc), table[b], n), oracle.paged_rows(f64(vc), table[b], n),
+                                128 ** -0.5)
+        assert np.allclose(out[b], want, rtol=0, atol=2.0 ** -14)
 
 
 def test_attention_many_sequences():
@@ -521,6 +556,63 @@ def test_logits_large_vocabulary_crosses_the_counted_chunks():
     out, ids = zmoe_adjust_logits(z, hist, frequency=torch.ones(1, device="cuda"))
     assert out[0, 0, at].tolist() == [2, 2, 2, 3, 3, 3, 3] and ids.item() == V - 2
     assert int((out != 0).sum()) == len(at) + 1
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_logits_lie_anywhere(dtype):
+    """Logits, biases and outputs that begin at any element, alike and unlike within 16 bytes."""
+    r = rnd(17)
+    T, N, V = 2, 3, 131
+    hist = dev(r.integers(0, V, (T, 20, N)).astype(np.int32))
+    rep = torch.full((T,), 1.5, device="cuda")
+    z0, b0 = dev(r.standard_normal((T, N, V)), dtype), dev(r.standard_normal((N, V)), F32)
+    want, want_ids = zmoe_adjust_logits(z0, hist, repetition=rep, bias=b0)
+    for zo in range(0, 9):
+        for oo in (zo, 3):
+            z, out = (torch.full((T * N * V + 16,), 7.0, dtype=dtype, device="cuda") for _ in range(2))
+            b = torch.zeros(N * V + 16, device="cuda")
+            zv, ov, bv = z[zo:zo + T * N * V].view(T, N, V), out[oo:oo + T * N * V].view(T, N, V), b[zo % 5:zo % 5 + N * V].view(N, V)
+            zv.copy_(z0)
+            bv.copy_(b0)
+            got, ids = zmoe_adjust_logits(zv, hist, repetition=rep, bias=bv, out=ov)
+            assert torch.equal(got, want) and torch.equal(ids, want_ids)
+            assert bool((out[:oo] == 7).all()) and bool((out[oo + T * N * V:] == 7).all())
+
+
+def test_logits_more_counted_ids_than_threads():
+    """Rows in place, counted in several chunks, with far more distinct ids in the history than a CTA has threads."""
+    r = rnd(18)
+    V, L = 60001, 3000
+    for dtype in (F32, BF16):
+        z = dev(r.standard_normal((2, 1, V)) * 3, dtype)
+        src = f64(z)
+        hist = r.integers(0, V, (2, L, 1)).astype(np.int32)
+        hist[:, :40] = np.arange(V - 40, V)[None, :, None]
+        hist[:, 40:80] = np.arange(40)[None, :, None]
+        rep, frq = np.full(2, 1.25, np.float32), np.full(2, 0.5, np.float32)
+        ok = r.random((2, 1, V)) < 0.6
+        out, ids = zmoe_adjust_logits(z, dev(hist), None, dev(rep), None, dev(frq), mask=dev(oracle.mask_bits(ok)), out=z)
+        want = oracle.adjust_logits(src, hist, None, rep, None, frq, allowed=ok)
+        got = f64(out)
+        assert np.array_equal(np.isneginf(got), ~ok)
+        w, g = np.where(ok, want, 0), np.where(ok, got, 0)
+        assert np.all(np.abs(g - w) <= 4 * 2.0 ** -24 * (2 * np.abs(src) + np.abs(w) + 2) + HALF[dtype] * 1.01 * np.abs(w))
+        assert np.array_equal(ids.cpu().numpy(), oracle.allowed_greedy(got, ok))
+
+
+def test_logits_that_are_all_lowest():
+    """Everything that is allowed is -inf or NaN: the lowest allowed -inf, listed or not, in any part of the row."""
+    inf = float("inf")
+    for V in (5, 300, 1025, 40001):
+        z = torch.full((2, 1, V), -inf, device="cuda")
+        z[0, 0, :3] = float("nan")
+        hist = dev(np.array([[[4]], [[1]]], np.int32))
+        ok = np.ones((2, 1, V), bool)
+        ok[1, 0, 0] = False
+        _, ids = zmoe_adjust_logits(z, hist, presence=torch.ones(2, device="cuda"), mask=dev(oracle.mask_bits(ok)))
+        assert ids.flatten().tolist() == [3, 1]
+        z[1] = float("nan")
+        assert zmoe_adjust_logits(z)[1].flatten().tolist() == [3, -1]
 
 
 def test_logits_bad_ids_are_counted():
