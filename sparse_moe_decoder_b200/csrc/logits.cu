@@ -9,7 +9,7 @@
 //
 // Bound by HBM for large vocabularies (logits read once, written once), by latency for one frame.  A row
 // (stream, codebook) is split over a cluster of 1 to 8 CTAs.  Each counts its ids' occurrences in shared memory
-// (16-bit counters, so up to 28160 ids a pass), passes over its logits once, and leaves its best (value, id) in
+// (16-bit counters, as many ids at a time as fit), passes over its logits once, and leaves its best (value, id) in
 // the first CTA's shared memory, which takes the largest: no workspace, one launch, and the order in which CTAs
 // finish does not matter.
 //
@@ -36,12 +36,9 @@ using namespace ptx;
 constexpr int kAhead = 2;           // vectors in flight a thread
 constexpr int kBlocks = 3;         // CTAs an SM, of 256 threads
 constexpr int kMaxSplit = 8;       // the portable cluster size
-constexpr int kChunk = 28160;      // ids counted at a time
 constexpr int kEnds = 32;          // ids at a row's two ends, at most 4 + 7 and 4 + 2 * 7
-constexpr int kEndVecs = 8;         // their vectors, rounded up
-constexpr int kMaxIds = kChunk + 8 * kEndVecs;
-constexpr int kMaxSmem = kMaxIds * 2 + kMaxIds / 8 + 4 + (kMaxIds + kEnds) * 6;   // counters, their bits, the list
-static_assert(kMaxSmem <= 226 * 1024, "one CTA an SM at least");
+constexpr int kEndVecs = 8;        // their vectors, rounded up
+constexpr int kMaxSmem = 224 * 1024;
 constexpr int kMaxHistory = 65535; // what a 16-bit counter holds
 
 struct AdjustArgs {
@@ -56,6 +53,7 @@ struct AdjustArgs {
   int N, V, L, split;
   int at_once;                // vectors counted at a time, beside those of the ends
   int list;                   // ids that can be listed, even
+  int in_place;               // out is logits
   int same;                   // logits and out lie alike within a vector
   unsigned int* errors;
 };
@@ -130,7 +128,7 @@ struct Row {
     constexpr int E = kE<TL>;
     f.x.load(src + v);
     f.ok = (1u << E) - 1;
-    if (mask) f.ok &= __funnelshift_r(*(mask + (v >> 5)), *(mask + ((v + E - 1) >> 5)), v & 31);
+    if (mask) f.ok &= __funnelshift_r(mask[v >> 5], mask[(v + E - 1) >> 5], v & 31);
     if (TURN >= 0) {
       const float4* p = reinterpret_cast<const float4*>(bias + v - TURN);
       float w[E + 4];
@@ -189,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks * 256 / kThreads) adjust_ker
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = static_cast<int>(threadIdx.x) + u * kThreads;
-    early[u] = counted && i < a.L ? *(hist + static_cast<size_t>(i) * a.N) : -1;
+    early[u] = counted && i < a.L ? hist[static_cast<size_t>(i) * a.N] : -1;
   }
   int len = 0;
   if (counted) {
@@ -246,22 +244,24 @@ __global__ void __launch_bounds__(kThreads, kBlocks * 256 / kThreads) adjust_ker
         for (int u = 0; u < 2; ++u)
           if (static_cast<int>(threadIdx.x) + u * kThreads < len) count(early[u]);
 #pragma unroll 4
-        for (int i = threadIdx.x + 2 * kThreads; i < len; i += kThreads) count(*(hist + static_cast<size_t>(i) * a.N));
+        for (int i = threadIdx.x + 2 * kThreads; i < len; i += kThreads) count(hist[static_cast<size_t>(i) * a.N]);
       }
       __syncthreads();
-      // the listed logits are read before the pass writes anything, for `out` may be `logits`
       const int n_listed = listed;
-      float lb = 0.f;
+      float lx = 0.f, lb = 0.f;
       bool lok = true;
-      auto ask = [&](int i) {   // the bias and the mask of a listed id
+      auto ask = [&](int i) {   // the logit, the bias and the mask of a listed id
         const int id = first + list_at[i];
+        if (!a.in_place) lx = as_float(r.src[id]);
         if (TURN >= 0) lb = r.bias[id];
-        if (r.mask) lok = (*(r.mask + (id >> 5)) >> (id & 31)) & 1u;
+        if (r.mask) lok = (r.mask[id >> 5] >> (id & 31)) & 1u;
       };
-#pragma unroll 2
-      for (int i = threadIdx.x; i < n_listed; i += kThreads) list_x[i] = as_float(r.src[first + list_at[i]]);
       if (static_cast<int>(threadIdx.x) < n_listed) ask(threadIdx.x);
-      if (n_listed) __syncthreads();
+      if (a.in_place && n_listed) {   // read before the pass writes anything
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n_listed; i += kThreads) list_x[i] = as_float(r.src[first + list_at[i]]);
+        __syncthreads();
+      }
       int best_at = -1, allowed_at = -1;   // the vector of this chunk's best, and the first that allows an id
       Vec<TL> best;
       auto rest_of = [&](int i) -> uint32_t {   // bits of the vector's ids that are not listed
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks * 256 / kThreads) adjust_ker
         if (i >= kThreads) ask(i);
         const int at = list_at[i], id = first + at;
         const uint32_t c = counted ? (counts[at >> 1] >> ((at & 1) * 16)) & 0xFFFFu : 0u;
-        float x = list_x[i];
+        float x = a.in_place ? list_x[i] : lx;
         if (c) {
           if (a.repetition) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
           if (a.frequency) x = __fsub_rn(x, __fmul_rn(frq, static_cast<float>(c)));
@@ -430,6 +430,7 @@ extern "C" zmoe_status zmoe_adjust_logits(const void* logits, zmoe_dtype dtype, 
   a.bias = bias; a.mask = mask; a.ids = ids;
   a.N = N; a.V = V; a.L = L;
   a.errors = device_error_counter();
+  a.in_place = out == logits;
   a.same = ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
   // as many CTAs as run at once, with at least 2048 ids each
   int split = 1;
@@ -439,12 +440,24 @@ extern "C" zmoe_status zmoe_adjust_logits(const void* logits, zmoe_dtype dtype, 
   const int E = dtype == ZMOE_BF16 ? 8 : 4;
   const int vecs = ((V + 2 * E - 2) / E + split - 1) / split;
   const int threads = vecs <= 2 * kAhead * 128 ? 128 : 256;   // short rows: smaller CTAs, so that more rows run at once
-  const int step = kAhead * threads, most = kChunk / E / step * step, chunks = (vecs + most - 1) / most;
-  a.at_once = ((vecs + chunks - 1) / chunks + step - 1) / step * step;
-  const int counters = E * (a.at_once + kEndVecs);
-  a.list = kEnds;
-  if (a.history) a.list += ((L < counters ? L : counters) + 1) & ~1;
-  const size_t smem = (a.history ? static_cast<size_t>(counters) * 2 + (counters + 31) / 32 * 4 : 0) + static_cast<size_t>(a.list) * 6;
+  // As few chunks as fit shared memory beside the other CTAs of an SM: each takes the history anew.
+  const int step = kAhead * threads;
+  const long long ctas = rows * split;
+  const int per_sm = ctas > 2LL * num_sms() ? 3 : (ctas > num_sms() ? 2 : 1);
+  size_t smem = 0;
+  for (int chunks = 1;; ++chunks) {
+    a.at_once = ((vecs + chunks - 1) / chunks + step - 1) / step * step;
+    a.list = kEnds;
+    if (!a.history) {
+      smem = static_cast<size_t>(a.list) * 6;
+      break;
+    }
+    const int counters = E * (a.at_once + kEndVecs);
+    a.list += ((L < counters ? L : counters) + 1) & ~1;
+    smem = static_cast<size_t>(counters) * 2 + (counters + 31) / 32 * 4 + static_cast<size_t>(a.list) * (a.in_place ? 6 : 2);
+    // a counter's number has 16 bits, in the list
+    if (counters <= 65536 && (smem <= kMaxSmem / per_sm || a.at_once == step)) break;
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int n = static_cast<int>(rows);
   if (threads == 128)
