@@ -752,3 +752,96 @@ def test_captured_and_replayed_with_new_inputs():
     want = one_step(b)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("before", ["nothing", "copy", "fill", "another stream", "two streams", "host copy", "event"])
+def test_captured_behind_anything(before):
+    """Each operator as the first call behind a copy, a memset, a fork, a join of two streams: captured, replayed with
+    other inputs, and right."""
+    def head(s, side, fresh):
+        if before == "copy":
+            s["h"].copy_(fresh["h"]); s["qkv"].copy_(fresh["qkv"]); s["z"].copy_(fresh["z"])
+        elif before == "fill":
+            for k in ("h", "qkv", "z"):
+                s[k].zero_()
+        elif before in ("another stream", "two streams"):
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                for k in ("h", "qkv", "z"):
+                    s[k].add_(1.0)
+            if before == "two streams":
+                s["delta"].mul_(1.0)
+            main.wait_stream(side)
+        elif before == "host copy":
+            s["h"].copy_(fresh["pinned"], non_blocking=True)
+        elif before == "event":
+            torch.cuda.Event().record()
+
+    def calls(s):
+        u = lambda a, b: s["qkv"][:, a * 64:b * 64].unflatten(1, (b - a, 64))  # noqa: E731
+        return dict(
+            norm=lambda: zmoe_add_rmsnorm(s["h"], s["gamma"], s["delta"], outs=s["n"]),
+            append=lambda: zmoe_kv_append(u(8, 10), u(10, 12), s["pos"], s["kc"], s["vc"], s["table"], q=u(0, 8),
+                                          inv_freq=s["inv"], q_out=s["q"]),
+            attn=lambda: zmoe_paged_attention(s["q"], s["kc"], s["vc"], s["table"], s["lens"], out=s["o"],
+                                              workspace=s["ws"]),
+            logits=lambda: zmoe_adjust_logits(s["z"], s["hist"], repetition=s["rep"], out=s["out"], ids=s["ids"]))
+
+    side = torch.cuda.Stream()
+    for op in ("norm", "append", "attn", "logits"):
+        a, b, fresh = step_inputs(31), step_inputs(31), step_inputs(32)
+        fresh["pinned"] = fresh["h"].cpu().pin_memory()
+        for s in (a, b):
+            s["q"].copy_(dev(rnd(3).standard_normal(s["q"].shape), BF16))
+        one_step(step_inputs(33))                                        # first use outside the capture
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            head(b, side, fresh)
+            calls(b)[op]()
+        for _ in range(3):
+            graph.replay()
+            head(a, side, fresh)
+            torch.cuda.synchronize()
+            calls(a)[op]()
+            torch.cuda.synchronize()
+        if op == "norm":
+            assert all(torch.equal(a["n"][k], b["n"][k]) for k in a["n"])
+        elif op == "append":
+            assert all(torch.equal(a[k], b[k]) for k in ("kc", "vc", "q"))
+        elif op == "attn":
+            assert torch.equal(a["o"], b["o"])
+        else:
+            assert torch.equal(a["out"], b["out"]) and torch.equal(a["ids"], b["ids"])
+        del graph
+
+
+def test_chains_without_waiting():
+    """Many dependent steps in a row, each kernel launched beside the one before it: as with a wait between all calls."""
+    def run(wait):
+        s = step_inputs(41)
+        s["lens"].copy_(s["pos"] + 1)
+        for i in range(60):
+            u = lambda a, b: s["qkv"][:, a * 64:b * 64].unflatten(1, (b - a, 64))  # noqa: E731
+            steps = [
+                lambda: zmoe_add_rmsnorm(s["h"], s["gamma"], s["delta"], outs=dict(h=s["h"], x=s["n"]["x"])),
+                lambda: zmoe_kv_append(u(8, 10), u(10, 12), s["pos"], s["kc"], s["vc"], s["table"], q=u(0, 8),
+                                       inv_freq=s["inv"], q_out=s["q"]),
+                lambda: zmoe_paged_attention(s["q"], s["kc"], s["vc"], s["table"], s["lens"], out=s["o"], workspace=s["ws"]),
+                # the next step's keys come from this step's output, its residual from the logits
+                lambda: zmoe_add_rmsnorm(s["o"].view(3, 512), s["ones"], outs=dict(x=s["qkv"][:, :512].contiguous())),
+                lambda: s["qkv"][:, :512].copy_(s["o"].view(3, 512)),
+                lambda: zmoe_adjust_logits(s["z"], s["hist"], repetition=s["rep"], out=s["z"], ids=s["ids"]),
+                lambda: s["pos"].sub_(1).clamp_(min=0),
+            ]
+            s.setdefault("ones", torch.ones(512, device="cuda"))
+            for f in steps:
+                f()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [s[k] for k in ("h", "kc", "vc", "o", "z", "ids", "q")]
+
+    a, b = run(True), run(False)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
