@@ -18,11 +18,11 @@
 // keeps both free of bank conflicts.  S leaves the first product in the layout that the second takes P^T in.  The
 // maximum and the sum of the softmax run along in registers.
 //
-// Work is split over the cache's length: the (sequence, group, 16-token tile) triples are one line of tiles,
-// cut into equal pieces, one a warp, so that ragged lengths balance; the ring runs ahead over the ends of
-// sequences.  A warp writes the groups that lie within its piece; of a group that is cut it leaves (maximum, sum, O)
-// in the workspace, and a second kernel, launched to start early (programmatic dependent launch), joins them in a
-// fixed order.
+// Work is split over the cache's length: the (sequence, group, 16-token tile) triples are one line of tiles, cut into
+// equal pieces, one a warp, so that ragged lengths balance; the ring runs ahead over the ends of sequences.  A warp
+// writes the groups that lie within its piece; of a group that is cut it leaves a part (maximum, sum, O).  Where groups
+// are cut into many, a CTA's warps take neighbouring pieces and join their parts first.  A second kernel, launched to
+// start early (programmatic dependent launch), joins what is left in a fixed order.
 //
 // Measured: 64 sequences of 1 to 4096 tokens (134k), 16 + 4 heads of 128, bf16: 54 us, 5.0 TB/s; 4 sequences, 286k
 // tokens, 32 + 4 heads of 128, E4M3: 63 us, 4.6 TB/s; one sequence of 431 tokens: 8.3 us.  A longer cache adds at 6.1
@@ -45,10 +45,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kJoinThreads = 256;
-constexpr int kMaxWarpsPerSm = 12;
+constexpr int kMaxWarps = 12;        // of a CTA of the first kernel
 constexpr uint64_t kWaitNs = 2000000000ull;   // a wait for a copy gives up after this
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -64,8 +62,10 @@ struct AttnArgs {
   int B, Hq, Hkv, G, gtiles, max_pages, n_pages, page_size;
   void* out;              // [B, Hq, D]
   float* lse;             // [B, Hq] or null
-  float* parts;           // [warps][2] of {m[H], l[H], O[H][D]}, H = 8 HT
-  int warps;              // warps of the first kernel
+  float* parts;           // [warps][2] of {m[H], l[H], O[H][D]}, H = 8 HT: what the first kernel leaves to the second;
+                          // or, where its CTAs join their warps' parts, [ctas][2], and behind them [warps] of the parts
+                          // that a warp is done with before its last one
+  int ctas;               // of the first kernel
   int together;           // query heads of a group that a block of the second kernel joins
   unsigned int *errors, *timeouts;
 };
@@ -119,15 +119,15 @@ __device__ __forceinline__ long long divide(long long x, long long y) {   // of 
   return x / y;
 }
 
-// `total` tiles in `count` pieces, one a warp, none empty: the first `more` pieces have one tile more.
+// `total` tiles in `count` pieces, none empty: the first `more` pieces have one tile more.
 struct Pieces {
   int count;
   long long size, more;
 
-  __device__ __forceinline__ Pieces(long long total, int warps)
-      : count(total < warps ? static_cast<int>(total) : warps), size(divide(total, count)), more(total - size * count) {}
+  __device__ __forceinline__ Pieces(long long total, int most)
+      : count(total < most ? static_cast<int>(total) : most), size(divide(total, count)), more(total - size * count) {}
   __device__ __forceinline__ long long start(long long w) const { return w * size + (w < more ? w : more); }
-  __device__ __forceinline__ int owner(long long x) const {   // the warp whose piece tile x is in
+  __device__ __forceinline__ int owner(long long x) const {   // the piece that tile x is in
     const long long big = more * (size + 1);
     return static_cast<int>(x < big ? divide(x, size + 1) : more + divide(x - big, size));
   }
@@ -155,6 +155,19 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long* scr
   return before + inc - mine;
 }
 
+// A part of a group (sequence b, group u) as a warp leaves it; null: none.
+struct Segment {
+  const float* part;
+  int b, u;
+  bool begins, ends;   // with the group's first tile, with its last
+};
+
+// Warps of a CTA of the first kernel, one CTA an SM: 168 or 255 registers a thread.
+template <int HT>
+__host__ __device__ constexpr int warps_of() {
+  return HT == 1 ? 12 : 8;
+}
+
 template <int D, int HT>
 __host__ __device__ constexpr int part_floats() {
   return 8 * HT * (D + 2);
@@ -173,10 +186,11 @@ struct Lay {
   static constexpr int half = 16 * row;            // bytes of a tile's keys or values
   static constexpr int tiles = 4096 / half;        // tiles of a step
   static constexpr int slot = 8192;                // bytes of a step: its keys, its values
-  static constexpr int blocks = HT == 1 ? 3 : 2;   // CTAs an SM: 168 or 255 registers a thread
+  static constexpr int warps = warps_of<HT>();
   static constexpr int slots = HT == 1 ? 2 : 3;
-  static constexpr int smem = kWarps * slots * slot + 1024;   // the ring starts on 1024 bytes
+  static constexpr int smem = warps * slots * slot + 1024;   // the rings start on 1024 bytes
   static_assert(half % 1024 == 0 && tiles >= 1, "whole swizzle atoms");
+  static_assert(part_floats<D, HT>() * 4 <= slots * slot && warps <= kMaxWarps, "a part fits the warp's ring");
 
   // Chunk c of lane j's share of a key row, in 16-byte chunks of the row: eight neighbouring lanes, which have two
   // rows, reach all banks.
@@ -233,11 +247,18 @@ __device__ __forceinline__ float gate_of(const AttnArgs& a, int b, int head) {
   return a.gate ? 1.f / (1.f + expf(-a.gate[static_cast<size_t>(b) * a.Hq + head])) : 1.f;
 }
 
+// Do the CTAs of the first kernel join the parts of their warps?  It costs every CTA 2 to 3 us at its end, and saves the
+// second kernel a factor of 12 (or 8) where a group is cut into many parts: 27 parts a group took 8.3 us a call without
+// and 9.6 with, 7 parts 54.6 and 57.2, 111 parts 65.5 and 61.6, 1250 parts 71 and 15.
+__device__ __forceinline__ bool joined_early(const AttnArgs& a, const Pieces& pieces) {
+  return pieces.count > 64LL * a.B * a.Hkv * a.gtiles;
+}
+
 template <int D, bool FP8, int HT, typename TO>
-__global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
+__global__ void __launch_bounds__(32 * Lay<D, FP8, HT>::warps, 1)
     attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a) {
   using L = Lay<D, FP8, HT>;
-  constexpr int H = 8 * HT;
+  constexpr int H = 8 * HT, kWarps = L::warps, kThreads = 32 * kWarps;
   constexpr int kTerms = !FP8 && sizeof(TO) == 4 ? 3 : 2;
   constexpr float kPScale = FP8 ? 32768.f : 1.f;   // f16 holds P in [0, 2^15]: weights down to 2^-39 survive
   extern __shared__ unsigned char ring_raw[];
@@ -245,10 +266,13 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
   __shared__ long long scan[kWarps];
   __shared__ int at_b[kWarps];
   __shared__ long long at_off[kWarps];
+  __shared__ Segment segments[2 * kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
   const int units = a.Hkv * a.gtiles;
   uint64_t* bar = bars[warp];
-  const uint32_t ring = ((smem_u32(ring_raw) + 1023u) & ~1023u) + static_cast<uint32_t>(warp * L::slots * L::slot);
+  unsigned char* const rings = ring_raw + ((1024u - (smem_u32(ring_raw) & 1023u)) & 1023u);
+  const uint32_t ring = smem_u32(rings) + static_cast<uint32_t>(warp * L::slots * L::slot);
+  if (lane < 2) segments[2 * warp + lane].part = nullptr;
   if (lane == 0) {
     asm volatile("prefetch.tensormap [%0];\n\tprefetch.tensormap [%1];" ::"l"(reinterpret_cast<uint64_t>(&kmap)),
                  "l"(reinterpret_cast<uint64_t>(&vmap)));
@@ -269,11 +293,16 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
   long long total;
   const long long pre = block_prefix<kWarps>(mine, scan, total);
   if (total == 0) return;
-  const Pieces pieces(total, a.warps);
+  const Pieces pieces(total, a.ctas * kWarps);
+  // neighbouring pieces go to a CTA that joins them, or to neighbouring SMs
+  const bool early = joined_early(a, pieces);
+  const int first_piece = early ? blockIdx.x * kWarps : blockIdx.x, next_piece = early ? 1 : a.ctas;
+  if (first_piece >= pieces.count) return;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const long long x = pieces.start(static_cast<long long>(blockIdx.x) * kWarps + w);
-    if (x >= pre && x < pre + mine) {
+    const int i = first_piece + w * next_piece;
+    const long long x = pieces.start(i);
+    if (i < pieces.count && x >= pre && x < pre + mine) {
       long long p = pre;
       int b = b_lo;
       for (;; ++b) {
@@ -286,11 +315,12 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
     }
   }
   __syncthreads();
-  const long long gw = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  if (gw >= pieces.count) return;
-  const int piece = static_cast<int>(pieces.start(gw + 1) - pieces.start(gw));   // tiles; 2^31 of them would take hours
-  int b = at_b[warp], n = seq_len(a, b), nt = tiles_of(n);
-  int u = static_cast<int>(divide(at_off[warp], nt)), tile = static_cast<int>(at_off[warp] - static_cast<long long>(u) * nt);
+  const int gw = first_piece + warp * next_piece;
+  const bool busy = gw < pieces.count;
+  const int piece = busy ? static_cast<int>(pieces.start(gw + 1) - pieces.start(gw)) : 0;   // tiles (2^31 would take hours)
+  int b = busy ? at_b[warp] : 0, n = seq_len(a, b), nt = tiles_of(n);
+  int u = busy ? static_cast<int>(divide(at_off[warp], nt)) : 0;
+  int tile = busy ? static_cast<int>(at_off[warp] - static_cast<long long>(u) * nt) : 0;
 
   // The feeder runs ahead of the products: the keys and values of a step's tiles into the next slot.
   const int tpp = a.page_size >> 4;   // tiles per page
@@ -610,7 +640,15 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
     // lane (g, j): o[h][..] has heads 8 h + 2 j (elements 0, 2) and + 1 (1, 3), columns v_col and + 1
     const bool whole = tile == 0 && t_end == nt;
     const int part_slot = todo == piece ? 0 : 1;
-    float* part = a.parts + (static_cast<size_t>(gw) * 2 + part_slot) * part_floats<D, HT>();
+    const bool last = todo == t_end - tile;
+    float* part;
+    if (early) {   // the last part lies in the ring, which is free then, one before it in memory
+      part = last ? reinterpret_cast<float*>(rings + warp * L::slots * L::slot)
+                  : a.parts + (static_cast<size_t>(a.ctas) * 2 + gw) * part_floats<D, HT>();
+      if (!whole && lane == 0) segments[2 * warp + part_slot] = Segment{part, b, u, tile == 0, t_end == nt};
+    } else {
+      part = a.parts + (static_cast<size_t>(gw) * 2 + part_slot) * part_floats<D, HT>();
+    }
     const float vs = FP8 ? a.v_scale[hk] / kPScale : 1.f;
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
@@ -663,11 +701,80 @@ __global__ void __launch_bounds__(kThreads, Lay<D, FP8, HT>::blocks)
       }
     }
   }
+  if (!early) return;
+  // The parts of the CTA's warps: those of one group follow one another.  A warp takes one head of one group at a time.
+  __syncthreads();
+  const Segment& own = segments[lane < 2 * kWarps ? lane : 0];
+  const uint32_t there = __ballot_sync(0xffffffffu, lane < 2 * kWarps && own.part != nullptr);
+  const bool opens = ((there >> lane) & 1u) && (own.begins || (there & ((1u << lane) - 1u)) == 0u);
+  const uint32_t starts = __ballot_sync(0xffffffffu, opens);
+  constexpr int kCols = D / 32;   // of a lane
+  for (int item = warp; item < __popc(starts) * H; item += kWarps) {
+    const int group = item / H, head = item - group * H;
+    uint32_t rest = starts;
+    for (int i = 0; i < group; ++i) rest &= rest - 1;
+    const int first = __ffs(rest) - 1;
+    const uint32_t later = rest & (rest - 1);   // the starts behind this one
+    const uint32_t mine_of = there & ~((1u << first) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
+    // lane s has the part of segment s
+    const bool has = (mine_of >> lane) & 1u;
+    const float mi = has ? own.part[head] : __int_as_float(0xff800000), li = has ? own.part[H + head] : 0.f;
+    float m = mi;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float weight = has ? pow2(mi - (m == __int_as_float(0xff800000) ? 0.f : m)) : 0.f;
+    const float l = warp_sum(li * weight);
+    float acc[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+    for (uint32_t left = mine_of; left;) {   // four parts at a time
+      float v[4][kCols], k[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = left ? __ffs(left) - 1 : first;
+        k[q] = __shfl_sync(0xffffffffu, weight, i);
+        if (!left) k[q] = 0.f;
+        left &= left - 1;
+        const float* p = segments[i].part + 2 * H + head * D + kCols * lane;
+        if (kCols == 4) {
+          const float4 w = *reinterpret_cast<const float4*>(p);
+          v[q][0] = w.x; v[q][1] = w.y; v[q][kCols - 2] = w.z; v[q][kCols - 1] = w.w;
+        } else {
+          const float2 w = *reinterpret_cast<const float2*>(p);
+          v[q][0] = w.x; v[q][1] = w.y;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (k[q] != 0.f) acc[c] = fmaf(v[q][c], k[q], acc[c]);   // an empty part's zeros meet no infinity
+    }
+    const Segment& seg = segments[first];
+    const int hk = seg.u / a.gtiles, hd = (seg.u - hk * a.gtiles) * H + head;
+    if (seg.begins && segments[31 - __clz(mine_of)].ends) {
+      if (hd >= a.G) continue;
+      const size_t at = static_cast<size_t>(seg.b) * a.Hq + static_cast<size_t>(hk) * a.G + hd;
+      const float f = l == 0.f ? 0.f : gate_of(a, seg.b, hk * a.G + hd) / l;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 2)
+        store2(static_cast<TO*>(a.out) + at * D + kCols * lane + c, acc[c] * f, acc[c + 1] * f);
+      if (a.lse && lane == 0) a.lse[at] = (m + log2f(l)) * kLn2;
+    } else {
+      float* part = a.parts + (static_cast<size_t>(blockIdx.x) * 2 + (first == 0 ? 0 : 1)) * part_floats<D, HT>();
+      if (lane == 0) {
+        part[head] = m;
+        part[H + head] = l;
+      }
+#pragma unroll
+      for (int c = 0; c < kCols; c += 2) store2(part + 2 * H + head * D + kCols * lane + c, acc[c], acc[c + 1]);
+    }
+  }
 }
 
 // Joins the parts of the groups that were cut and writes the rows of empty sequences.
 template <int D, int HT, typename TO>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(AttnArgs a) {
   constexpr int H = 8 * HT, kJoinWarps = kJoinThreads / 32, kLanes = D / 4, kRows = kJoinThreads / kLanes;
   __shared__ long long scan[kJoinWarps];
   __shared__ long long start_of_b;
@@ -705,11 +812,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
     return;
   }
   const long long p0 = start_of_b + static_cast<long long>(hk * a.gtiles + gt) * nt;
-  const Pieces pieces(total, a.warps);
-  const int w0 = pieces.owner(p0), parts = pieces.owner(p0 + nt - 1) - w0 + 1;
+  constexpr int kWarps = warps_of<HT>();
+  const Pieces pieces(total, a.ctas * kWarps);
+  const int span = joined_early(a, pieces) ? kWarps : 1;   // pieces that share parts
+  const int w0 = pieces.owner(p0) / span, parts = pieces.owner(p0 + nt - 1) / span - w0 + 1;
   if (parts == 1) return;   // written whole
   const float* base = a.parts + static_cast<size_t>(w0) * 2 * part_floats<D, HT>();
-  const int first_slot = pieces.start(w0) == p0 ? 0 : 1;
+  const int first_slot = pieces.start(w0 * span) == p0 ? 0 : 1;
   auto part_of = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? first_slot : 0)) * part_floats<D, HT>(); };
   // The first kernel's grid is done, and its writes are visible, behind this line.  What comes next is not let in
   // early: the blocks of the next step's first kernel fill the machine, and came to lie unevenly beside these (64 to
@@ -782,9 +891,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
 template <int D, bool FP8, int HT, typename TO>
 zmoe_status launch(AttnArgs a, cudaStream_t s) {
   using L = Lay<D, FP8, HT>;
-  static_assert(L::blocks * kWarps <= kMaxWarpsPerSm, "the workspace holds the warps' parts");
-  const int blocks = num_sms() * L::blocks;
-  a.warps = blocks * kWarps;
+  a.ctas = num_sms();
   // the cache as rows of one or two lines of 128 bytes (two rows of an 8-bit cache of 64 columns are a line)
   const cuuint32_t lines = L::row == 256 ? 2 : 1, tall = L::row == 64 ? 8 : 16;
   const cuuint64_t rows = static_cast<cuuint64_t>(a.n_pages) * a.Hkv * a.page_size * tall / 16;
@@ -796,8 +903,8 @@ zmoe_status launch(AttnArgs a, cudaStream_t s) {
     return fail(ZMOE_ERR_CUDA, "zmoe_paged_attention: the cache's tensor map cannot be made");
   if (cudaFuncSetAttribute(attn_kernel<D, FP8, HT, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem) != cudaSuccess)
     return check_launch("zmoe_paged_attention: shared memory attribute");
-  const zmoe_status st = launch_behind("zmoe_paged_attention", attn_kernel<D, FP8, HT, TO>, dim3(blocks), dim3(kThreads),
-                                       L::smem, s, 1, km, vm, a);
+  const zmoe_status st = launch_behind("zmoe_paged_attention", attn_kernel<D, FP8, HT, TO>, dim3(a.ctas),
+                                       dim3(32 * L::warps), L::smem, s, 1, km, vm, a);
   if (st != ZMOE_OK) return st;
   // A block a head, unless they are more than run at once: then it takes up to 8 heads of a group.
   a.together = 1;
@@ -830,7 +937,7 @@ size_t zmoe_paged_attention_workspace_size(int B, int Hq, int Hkv, int D) {
   using namespace zmoe;
   if (B <= 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
   const int H = Hq / Hkv <= 8 ? 8 : 16;
-  return static_cast<size_t>(num_sms()) * kMaxWarpsPerSm * 2 * H * (D + 2) * 4;
+  return static_cast<size_t>(num_sms()) * kMaxWarps * 2 * H * (D + 2) * 4;
 }
 
 zmoe_status zmoe_paged_attention(const void* q, const void* k_cache, const void* v_cache, zmoe_dtype kv_dtype,
