@@ -66,7 +66,7 @@ struct AttnArgs {
                           // or, where its CTAs join their warps' parts, [ctas][2], and behind them [warps] of the parts
                           // that a warp is done with before its last one
   int ctas;               // of the first kernel
-  int together;           // query heads of a group that a block of the second kernel joins
+  int together;           // log2 of the query heads of a group that a block of the second kernel joins
   unsigned int *errors, *timeouts;
 };
 
@@ -776,34 +776,62 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, HT>::warps, 1)
 template <int D, int HT, typename TO>
 __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(AttnArgs a) {
   constexpr int H = 8 * HT, kJoinWarps = kJoinThreads / 32, kLanes = D / 4, kRows = kJoinThreads / kLanes;
-  __shared__ long long scan[kJoinWarps];
-  __shared__ long long start_of_b;
+  __shared__ long long sums[2][kJoinWarps];
   __shared__ float red_m[kRows], red_l[kRows];
   __shared__ float4 red[kRows][kLanes];
   // D / 4 lanes have one head and every `ways`-th of its parts
-  const int per_group = (a.G + a.together - 1) / a.together, ways = kRows / a.together;
+  const int per_group = (a.G + (1 << a.together) - 1) >> a.together;
+  const int ways_log2 = (kRows == 8 ? 3 : 4) - a.together, ways = 1 << ways_log2;
   const int group = blockIdx.x / per_group, b = group / a.Hkv, hk = group - b * a.Hkv;
-  const int col = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
-  const int in_group = (blockIdx.x - group * per_group) * a.together + row / ways;   // heads of a block share a tile
-  const int gt = in_group / H, head = in_group - gt * H, hq = hk * a.G + in_group, first = row % ways;
+  const int col = threadIdx.x % kLanes, row = threadIdx.x / kLanes, first = row & (ways - 1);
+  const int in_group = ((blockIdx.x - group * per_group) << a.together) + (row >> ways_log2);   // heads of a block share a tile
+  const int gt = in_group / H, head = in_group - gt * H, hq = hk * a.G + in_group;
   const bool real = in_group < a.G;
-  const int units = a.Hkv * a.gtiles;
-  const int per = (a.B + kJoinThreads - 1) / kJoinThreads, b_lo = threadIdx.x * per;
-  const int b_hi = b_lo + per < a.B ? b_lo + per : a.B;
-  long long mine = 0;
-  for (int i = b_lo; i < b_hi; ++i) mine += static_cast<long long>(tiles_of(seq_len<true>(a, i))) * units;
-  long long total;
-  const long long pre = block_prefix<kJoinWarps>(mine, scan, total);
-  if (b >= b_lo && b < b_hi) {
-    long long p = pre;
-    for (int i = b_lo; i < b; ++i) p += static_cast<long long>(tiles_of(seq_len<true>(a, i))) * units;
-    start_of_b = p;
+  // the tiles of all sequences, and of those before this one
+  const int units = a.Hkv * a.gtiles, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long total = 0, before = 0;
+  for (int i = threadIdx.x; i < a.B; i += kJoinThreads) {
+    const int t = tiles_of(seq_len<true>(a, i));
+    total += t;
+    if (i < b) before += t;
+  }
+  const int nt = tiles_of(seq_len<true>(a, b));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (lane == 0) {
+    sums[0][warp] = total;
+    sums[1][warp] = before;
   }
   __syncthreads();
-  const int nt = tiles_of(seq_len<true>(a, b));
+  total = before = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    total += sums[0][w];
+    before += sums[1][w];
+  }
+  total *= units;
+  const long long p0 = before * units + static_cast<long long>(hk * a.gtiles + gt) * nt;
+  constexpr int kWarps = warps_of<HT>();
+  int w0 = 0, parts = 0, first_slot = 0;
+  if (nt > 0) {
+    const Pieces pieces(total, a.ctas * kWarps);
+    const bool early = joined_early(a, pieces);
+    const int x = pieces.owner(p0), y = pieces.owner(p0 + nt - 1);
+    w0 = early ? x / kWarps : x;
+    parts = (early ? y / kWarps : y) - w0 + 1;
+    first_slot = pieces.start(early ? w0 * kWarps : w0) == p0 ? 0 : 1;
+  }
   TO* out = static_cast<TO*>(a.out) + (static_cast<size_t>(b) * a.Hq + hq) * D;
-  if (nt == 0) {   // the first kernel does not touch these rows, and it began behind what came before both
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float* base = a.parts + static_cast<size_t>(w0) * 2 * part_floats<D, HT>();
+  auto part_of = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? first_slot : 0)) * part_floats<D, HT>(); };
+  // The first kernel's grid is done, and its writes are visible, behind this line; every block passes it, for what
+  // comes next begins when this grid ends.  It is not let in early: the blocks of the next step's first kernel fill the
+  // machine, and came to lie unevenly beside these (64 to 77 us a call at 286k E4M3 tokens).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (nt == 0) {   // the first kernel does not touch these rows
     if (real && first == 0) {
       store2(out + 4 * col, 0.f, 0.f);
       store2(out + 4 * col + 2, 0.f, 0.f);
@@ -811,19 +839,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(AttnArgs a) {
     }
     return;
   }
-  const long long p0 = start_of_b + static_cast<long long>(hk * a.gtiles + gt) * nt;
-  constexpr int kWarps = warps_of<HT>();
-  const Pieces pieces(total, a.ctas * kWarps);
-  const int span = joined_early(a, pieces) ? kWarps : 1;   // pieces that share parts
-  const int w0 = pieces.owner(p0) / span, parts = pieces.owner(p0 + nt - 1) / span - w0 + 1;
   if (parts == 1) return;   // written whole
-  const float* base = a.parts + static_cast<size_t>(w0) * 2 * part_floats<D, HT>();
-  const int first_slot = pieces.start(w0 * span) == p0 ? 0 : 1;
-  auto part_of = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? first_slot : 0)) * part_floats<D, HT>(); };
-  // The first kernel's grid is done, and its writes are visible, behind this line.  What comes next is not let in
-  // early: the blocks of the next step's first kernel fill the machine, and came to lie unevenly beside these (64 to
-  // 77 us a call at 286k E4M3 tokens).
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kBatch = 8;   // parts in flight, with a running maximum
   float m = __int_as_float(0xff800000), l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -907,12 +923,10 @@ zmoe_status launch(AttnArgs a, cudaStream_t s) {
                                        dim3(32 * L::warps), L::smem, s, 1, km, vm, a);
   if (st != ZMOE_OK) return st;
   // A block a head, unless they are more than run at once: then it takes up to 8 heads of a group.
-  a.together = 1;
-  while (static_cast<long long>(a.B) * a.Hkv * ((a.G + a.together - 1) / a.together) > 3LL * num_sms() &&
-         a.together < 8 && a.together < a.G)
-    a.together *= 2;
-  return launch_behind("zmoe_paged_attention (join)", join_kernel<D, HT, TO>,
-                       dim3(static_cast<unsigned>(a.B) * a.Hkv * ((a.G + a.together - 1) / a.together)),
+  a.together = 0;
+  auto join_blocks = [&]() { return static_cast<long long>(a.B) * a.Hkv * ((a.G + (1 << a.together) - 1) >> a.together); };
+  while (join_blocks() > 3LL * num_sms() && a.together < 3 && (1 << a.together) < a.G) ++a.together;
+  return launch_behind("zmoe_paged_attention (join)", join_kernel<D, HT, TO>, dim3(static_cast<unsigned>(join_blocks())),
                        dim3(kJoinThreads), 0, s, 1, a);
 }
 
