@@ -24,9 +24,10 @@
 // are cut into many, a CTA's warps take neighbouring pieces and join their parts first.  A second kernel, launched to
 // start early (programmatic dependent launch), joins what is left in a fixed order.
 //
-// Measured: 64 sequences of 1 to 4096 tokens (134k), 16 + 4 heads of 128, bf16: 54 us, 5.0 TB/s; 4 sequences, 286k
-// tokens, 32 + 4 heads of 128, E4M3: 63 us, 4.6 TB/s; one sequence of 431 tokens: 8.3 us.  A longer cache adds at 6.1
-// (bf16) and 7 TB/s (E4M3); about 12 us are the two launches, the lengths' prefix, the first copies and the join.
+// Measured: 64 sequences of 1 to 4096 tokens (134k), 16 + 4 heads of 128, bf16: 55 us, 5.0 TB/s; 4 sequences, 286k
+// tokens, 32 + 4 heads of 128, E4M3: 61 us, 4.8 TB/s; one sequence of 431 tokens: 8.4 us; one of 20000 with 8 + 1 heads:
+// 14.8 us.  A longer cache adds at 6.1 (bf16) and 7 TB/s (E4M3); about 12 us are the two launches, the lengths' prefix,
+// the first copies and the join.
 //
 // P is split into 16-bit terms, P = P_1 + P_2 (+ P_3), and the second product runs for each: one bf16 term alone would
 // cost 2^-9 of every weight.  Two bf16 terms leave 2^-16 of it, which a bf16 output does not show; an f32 output takes

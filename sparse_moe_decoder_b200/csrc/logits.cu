@@ -15,14 +15,18 @@
 //
 // The pass takes a vector of 16 bytes at an aligned address a thread at a time, two such vectors in flight; the
 // first ones are on their way before the counting starts.  Rows of odd length start anywhere in a vector, so a
-// vector's ids begin at E i - shift and the counters are laid out by id + shift; the ids of a row's
-// first and last vectors go one by one, so nothing outside the row is touched.  How the bias lies against the logits is the same for a
-// whole row, and the pass is compiled for each of the four ways (choosing the biases by it in the loop took three
+// vector's ids begin at E i - shift and the counters are laid out by id + shift; the ids of a row's first and last
+// vectors go one by one, so nothing outside the row is touched.  How the bias lies against the logits is the same for
+// a whole row, and the pass is compiled for each of the four ways (choosing the biases by it in the loop took three
 // instructions an id).
 //
 // The pass leaves out the ids that were counted.  Few as they are, most warps hold one of them, and would take
 // every step of the penalties for it; instead each is listed when its count leaves zero, as the ids at the ends are,
 // and a thread of its own takes it.
+//
+// Measured: 9 x 1025, 128 frames: 3.9 us a call; 576 rows of 1025 with 512 frames and masks: 7.0 us; 192 x 100003 bf16
+// with 2048 entries and masks: 45 us, of which the pass alone is 21.5 (a plain copy of these rows takes 19.7), biases and
+// masks 9, counting and settling 14 (102 us with the penalties within the pass).
 #include <type_traits>
 
 #include "sm100_ptx.cuh"
