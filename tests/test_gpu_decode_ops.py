@@ -459,6 +459,29 @@ def test_attention_nan_and_infinite_data_reach_their_rows_only():
     assert np.isposinf(out[1, :, 7]).all() and np.isfinite(np.delete(out[1], 7, 1)).all() and np.isfinite(out[2]).all()
 
 
+@pytest.mark.parametrize("lens", [[20000], [300, 20000, 0, 5000]])
+def test_attention_infinite_values_in_a_long_cache(lens):
+    """Groups cut into many parts: an infinity stays in its column, a NaN key in its sequence."""
+    r = rnd(19)
+    n = sum(-(-x // 64) for x in lens)
+    kc, vc, _, _ = make_cache(r, n, 1, 64, 128, "bf16")
+    need = [-(-x // 64) for x in lens]
+    table = np.zeros((len(lens), max(need)), np.int32)
+    ids, at = r.permutation(n), 0
+    for b, x in enumerate(need):
+        table[b, :x] = ids[at:at + x]
+        at += x
+    long = lens.index(20000)
+    vc[table[long, 200], 0, 13, 77] = float("-inf")
+    q = dev(r.standard_normal((len(lens), 6, 128)), BF16)
+    out = f64(zmoe_paged_attention(q, kc, vc, dev(table), dev(np.array(lens, np.int32))))
+    assert np.isneginf(out[long, :, 77]).all() and np.isfinite(np.delete(out[long], 77, 1)).all()
+    assert np.isfinite(np.delete(out, long, 0)).all()
+    kc[table[long, 3], 0, 5, 0] = float("nan")
+    out = f64(zmoe_paged_attention(q, kc, vc, dev(table), dev(np.array(lens, np.int32))))
+    assert np.isnan(out[long]).all() and np.isfinite(np.delete(out, long, 0)).all()
+
+
 def test_attention_is_repeatable_and_its_workspace_needs_no_clearing():
     r = rnd(13)
     lens = np.array([900, 77, 4000, 1], np.int32)
