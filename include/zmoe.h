@@ -430,6 +430,12 @@ ZMOE_API zmoe_status zmoe_decode_stack(const zmoe_stack_layer* layers, int n_lay
                                        void* layer_x, void* workspace, size_t ws_bytes, zmoe_stream_t stream);
 
 /*
+ * The four calls from here to zmoe_adjust_logits are the rest of a decode step around the MoE layer.  Their kernels are
+ * launched behind the one before them on `stream` (programmatic dependent launch): they may be scheduled while it still
+ * runs, and touch no memory before it is complete.  They order like any other launch, in captured graphs too.
+ */
+
+/*
  * The residual addition, the RMSNorm of the sum and its 8-bit codes in one pass ([DIGEST] item 5: pre-norm
  * residual blocks; the ZONOS2 page of the sglang-omni cookbook, "Benchmark Results": the served model runs fp8):
  *   h'[t] = h[t] + delta[t]                                   (fp32 sum, rounded to h_dtype; delta NULL: h' = h)

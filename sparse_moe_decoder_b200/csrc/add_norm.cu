@@ -250,6 +250,8 @@ extern "C" zmoe_status zmoe_add_rmsnorm(const void* h, zmoe_dtype h_dtype, const
                    (!x || aligned16(x)) && (!codes || aligned16(codes)) &&
                    (reinterpret_cast<uintptr_t>(scales) & 3u) == 0,
                "zmoe_add_rmsnorm: pointers must be 16-byte aligned (scales: 4-byte)");
+  ZMOE_REQUIRE(!delta || h_out != delta || h_dtype == delta_dtype,
+               "zmoe_add_rmsnorm: h_out may be delta only where their types are one");
   if (d > kMaxD) return fail(ZMOE_ERR_UNSUPPORTED, "zmoe_add_rmsnorm: d must be at most 32768");
   clear_error();
   const AddNormArgs a{h, delta, gamma, eps, 1.f / static_cast<float>(d), T, d, group, h_out, x, codes, scales};

@@ -93,7 +93,7 @@ def _norm(L, h=A, ht=F32, delta=A2, dt=F32, gamma=A3, eps=1e-6, T=4, d=256, ho=A
     dict(T=-1), dict(d=12), dict(d=0), dict(d=-8), dict(ht=2), dict(dt=7), dict(xt=2), dict(eps=-1.0),
     dict(eps=float("nan")), dict(h=NULL), dict(gamma=NULL), dict(group=64), dict(group=128, d=264), dict(h=A + 4),
     dict(delta=A + 8), dict(codes=A + 8), dict(scales=A + 2), dict(codes=NULL), dict(scales=NULL),
-    dict(ho=NULL, x=NULL, codes=NULL, scales=NULL),
+    dict(ho=NULL, x=NULL, codes=NULL, scales=NULL), dict(ho=A2, dt=BF16), dict(ho=A2, ht=BF16),
 ])
 def test_add_rmsnorm_refusals(L, kw):
     assert _norm(L, **kw) == 1
