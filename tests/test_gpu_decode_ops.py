@@ -543,6 +543,20 @@ def test_logits_each_step_may_be_left_out(off):
     logits_case(7, 2, 3, 500, 30, F32, **{off: False})
 
 
+def test_logits_many_middling_rows():
+    """More rows than run at once, of a length that goes either way: the same as a few of them alone."""
+    r = rnd(23)
+    z = dev(r.standard_normal((100, 5, 3001)) * 3, F32)
+    hist = dev(r.integers(0, 3001, (100, 70, 5)).astype(np.int32))
+    rep, bias = dev(r.uniform(1, 2, 100), F32), dev(r.standard_normal((5, 3001)), F32)
+    ok = dev(oracle.mask_bits(r.random((100, 5, 3001)) < 0.7))
+    out, ids = zmoe_adjust_logits(z, hist, repetition=rep, bias=bias, mask=ok)
+    for i in (0, 57, 99):
+        o, j = zmoe_adjust_logits(z[i:i + 1], hist[i:i + 1], repetition=rep[i:i + 1], bias=bias, mask=ok[i:i + 1])
+        assert torch.equal(o[0], out[i]) and torch.equal(j[0], ids[i])
+    logits_case(24, 100, 5, 3001, 40, F32)
+
+
 def test_logits_penalties_alone_and_none():
     logits_case(8, 2, 2, 300, 9, BF16, rep=False, frq=False, bias=False, mask=False, lens=False)
     z = dev(rnd(3).standard_normal((2, 2, 77)), F32)
