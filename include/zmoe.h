@@ -465,6 +465,7 @@ ZMOE_API zmoe_status zmoe_add_rmsnorm(const void* h, zmoe_dtype h_dtype, const v
  *     with (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved != 0
  *   row p % page_size of page page_table[s, p / page_size] receives the key and the value (rounded once, to bf16,
  *   or to E4M3 codes of value * fp32(1 / scale of the key-value head), saturating at 448); q_out the query.
+ *   q_out and the caches overlap no input.
  *   q: [T, Hq, D] or NULL, k, v: [T, Hkv, D], of in_dtype (f32 or bf16): heads contiguous, tokens q_stride,
  *   k_stride and v_stride elements apart (multiples of 16 bytes), so that they may lie in one packed projection.
  *   inv_freq: f64 [rotary_dim / 2] (NULL when rotary_dim == 0): the angle is reduced in 64 bits.

@@ -882,3 +882,43 @@ def test_chains_without_waiting():
 
     a, b = run(True), run(False)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_back_to_back_in_place():
+    """The same operator on its own output many times over, with nothing in between: what the kernel before wrote is what
+    is read, also where rows of different blocks share cache lines."""
+    r = rnd(51)
+    h0, gamma = dev(r.standard_normal((6000, 24)), F32), torch.ones(24, device="cuda")
+    delta = dev(r.standard_normal((6000, 24)), F32)
+    z0 = dev(r.standard_normal((301, 3, 1027)), F32)
+    bias = dev(r.standard_normal((3, 1027)), F32)
+    kc0, vc0, _, _ = make_cache(r, 40, 2, 16, 64, "bf16")
+    table, pos = dev(r.permutation(40).reshape(8, 5).astype(np.int32)), dev(np.array([70, 3, 66, 50, 0, 79, 31, 16], np.int32))
+    kv = dev(r.standard_normal((8, 2, 64)), BF16)
+    ws = torch.empty(zmoe_paged_attention_workspace_size(8, 2, 2, 64), dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        h, z, kc, vc, x, y = h0.clone(), z0.clone(), kc0.clone(), vc0.clone(), kv.clone(), torch.empty_like(kv)
+        lens = pos + 1
+        torch.cuda.synchronize()
+        for i in range(200):
+            zmoe_add_rmsnorm(h, gamma, delta, outs=dict(h=h))
+            if wait:
+                torch.cuda.synchronize()
+        for i in range(200):
+            zmoe_adjust_logits(z, bias=bias, out=z)
+            if wait:
+                torch.cuda.synchronize()
+        for i in range(200):   # the output of one step is the next one's query, key and value
+            zmoe_kv_append(x, x, pos, kc, vc, table, q=x, q_out=y)
+            if wait:
+                torch.cuda.synchronize()
+            zmoe_paged_attention(y, kc, vc, table, lens, out=x, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return h, z, kc, vc, x
+
+    want = run(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want, run(False)))
