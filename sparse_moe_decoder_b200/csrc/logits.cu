@@ -458,22 +458,22 @@ extern "C" zmoe_status zmoe_adjust_logits(const void* logits, zmoe_dtype dtype, 
   // against 9.4), up to 1024 where not all rows run at once anyway (1809 rows of 4039 f32: 18.3 against 26.5; one row of
   // 6000: 5.9 against 5.4; 512 rows of 12000 bf16: 21.7 against 16.5).
   const int threads = vecs <= 512 || (vecs <= 1024 && rows * split > static_cast<long long>(kBlocks) * num_sms()) ? 128 : 256;
-  // As few chunks as fit shared memory beside the other CTAs of an SM: each takes the history anew.
+  // As few chunks as fit shared memory beside the other CTAs of an SM (each takes the history anew) and a list of 16 bits.
   const int step = kAhead * threads;
   const long long ctas = rows * split;
   const int per_sm = ctas > 2LL * num_sms() ? 3 : (ctas > num_sms() ? 2 : 1);
   size_t smem = 0;
   for (int chunks = 1;; ++chunks) {
     a.at_once = ((vecs + chunks - 1) / chunks + step - 1) / step * step;
-    a.list = kEnds;
-    if (!a.history) {
-      smem = static_cast<size_t>(a.list) * 6;
-      break;
-    }
     const int counters = E * (a.at_once + kEndVecs);
-    a.list += ((L < counters ? L : counters) + 1) & ~1;
-    smem = static_cast<size_t>(counters) * 2 + (counters + 31) / 32 * 4 + static_cast<size_t>(a.list) * (a.in_place ? 6 : 2);
-    // a counter's number has 16 bits, in the list
+    a.list = kEnds;
+    if (a.history) {
+      a.list += ((L < counters ? L : counters) + 1) & ~1;
+      smem = static_cast<size_t>(counters) * 2 + (counters + 31) / 32 * 4 + static_cast<size_t>(a.list) * (a.in_place ? 6 : 2);
+    } else {
+      smem = static_cast<size_t>(a.list) * 6;
+    }
+    // a listed id is its place in the chunk, in 16 bits: with a history or without, a chunk has no more places
     if (counters <= 65536 && (smem <= kMaxSmem / per_sm || a.at_once == step)) break;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

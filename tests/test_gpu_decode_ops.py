@@ -922,3 +922,42 @@ def test_back_to_back_in_place():
     want = run(True)
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(want, run(False)))
+
+
+# 65536 ids is what 16 bits number: rows just below and above that many a CTA, in clusters of 1, 2 and 8 CTAs
+LONG_ROWS = [(230, 65472, BF16), (230, 65530, BF16), (230, 65536, BF16), (230, 65543, BF16), (256, 128256, BF16),
+             (112, 151936, BF16), (288, 65539, F32), (288, 70000, F32), (223, 100003, F32), (1, 524289, F32),
+             (1, 600000, F32), (2, 600011, BF16)]
+
+
+@pytest.mark.parametrize("rows,V,dtype", LONG_ROWS)
+@pytest.mark.parametrize("how", ["out", "in place", "history only"])
+def test_logits_of_long_rows_without_penalties(rows, V, dtype, how):
+    """Every id is written, those at a row's end too, and the greedy id is found among them."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.randn((rows, 1, V), generator=g, device="cuda").to(dtype)
+    bias = torch.randn((1, V), generator=g, device="cuda")
+    at = V - 1 - torch.arange(rows, device="cuda") % 12                  # the largest logit: one of the last ids
+    z[torch.arange(rows, device="cuda"), 0, at] = 64.0
+    want = (z.float() + bias).to(dtype)                                  # one fp32 sum, one rounding
+    best = want.float().amax(2, keepdim=True)
+    want_ids = torch.where(want == best, torch.arange(V, device="cuda"), V).amin(2).int()
+    out = z if how == "in place" else torch.full_like(z, 1000.0)
+    hist = torch.zeros((rows, 3, 1), dtype=torch.int32, device="cuda") if how == "history only" else None
+    got, ids = zmoe_adjust_logits(z, hist, bias=bias, out=out)
+    assert torch.equal(got, want) and torch.equal(ids, want_ids) and torch.equal(ids[:, 0], at.int())
+
+
+def test_logits_of_long_rows_with_masks_and_no_bias():
+    """The same with a mask that leaves only ids at the ends, and with one that leaves none."""
+    rows, V = 300, 131075
+    z = torch.randn((rows, 1, V), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(BF16)
+    words = torch.zeros((rows, 1, (V + 31) // 32), dtype=torch.int32, device="cuda")
+    words[:100, 0, -1] = 0b100                                           # id V - 1 alone
+    words[100:200, 0, 0] = 0b10                                          # id 1 alone
+    out, ids = zmoe_adjust_logits(z, mask=words, out=torch.full_like(z, 1000.0))
+    assert ids.flatten().tolist() == [V - 1] * 100 + [1] * 100 + [-1] * 100
+    ok = torch.zeros((rows, 1, V), dtype=torch.bool, device="cuda")
+    ok[:100, 0, V - 1] = True
+    ok[100:200, 0, 1] = True
+    assert torch.equal(out, torch.where(ok, z, float("-inf")))
