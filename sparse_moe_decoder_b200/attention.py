@@ -41,7 +41,8 @@ class PagedCache:
     """Keys and values of ``n_seqs`` sequences in pages, for ``n_layers`` layers that share one page table.
 
     dtype torch.bfloat16, or torch.uint8 for E4M3 codes with k_scale, v_scale f32 [n_layers, Hkv].  Pages are handed
-    out by ``reserve`` and taken back by ``release``; ``advance`` gives every sequence its next position."""
+    out by ``reserve`` and taken back by ``release``; ``advance`` gives every sequence its next position.  ``lens`` counts
+    cached tokens only: it never passes ``room``, the tokens that a sequence's pages hold."""
 
     def __init__(self, n_layers: int, n_seqs: int, max_len: int, Hkv: int, D: int, page_size: int = 16,
                  n_pages: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
@@ -59,6 +60,7 @@ class PagedCache:
         self.table = torch.full((n_seqs, cols), -1, dtype=torch.int32, device=device)
         self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=device)   # cached tokens
         self.pos = torch.zeros(n_seqs, dtype=torch.int32, device=device)    # the step's positions
+        self.room = torch.zeros(n_seqs, dtype=torch.int32, device=device)   # tokens that the reserved pages hold
         self.free: List[int] = list(range(self.n_pages - 1, -1, -1))
         self.pages: List[List[int]] = [[] for _ in range(n_seqs)]
 
@@ -76,6 +78,7 @@ class PagedCache:
             new = [self.free.pop() for _ in range(need - have)]
             self.pages[s] += new
             self.table[s, have:need] = torch.tensor(new, dtype=torch.int32)
+            self.room[s] = need * self.page_size
 
     def release(self, seq: int) -> None:
         """Takes a sequence's pages back; it starts again at position 0."""
@@ -83,13 +86,16 @@ class PagedCache:
         self.pages[seq] = []
         self.table[seq].fill_(-1)
         self.lens[seq].zero_()
+        self.room[seq].zero_()
 
     def advance(self, stream=None) -> None:
         """One more token for every sequence: its position in ``pos``, its new length in ``lens``.  A position
-        without a reserved page counts a device error when the token is stored, and the token is lost."""
+        without a reserved page counts a device error when the token is stored, and the token is lost: the length
+        stays, so that a page that comes later holds no row that was never stored."""
         with torch.cuda.stream(stream):
             self.pos.copy_(self.lens)
             self.lens.add_(1)
+            torch.minimum(self.lens, self.room, out=self.lens)
 
     def layer(self, i: int) -> dict:
         """The cache arguments of zmoe_kv_append and zmoe_paged_attention for layer ``i``."""

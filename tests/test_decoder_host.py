@@ -52,3 +52,28 @@ def test_the_window_keeps_the_last_frames():
     assert sorted(r.history[1, :, 2].tolist()) == [2, 3, 4, 5]
     with pytest.raises(ValueError):
         LogitRules(1, 1, 0, device="cpu")
+
+
+def test_a_released_sequence_starts_again_though_others_went_on():
+    c = PagedCache(1, 2, 32, 1, 64, 16, device="cpu")
+    c.reserve(16)
+    for _ in range(5):
+        c.advance()
+    c.release(0)
+    for _ in range(5):
+        c.advance()
+    assert c.lens.tolist() == [0, 10] and c.pos.tolist() == [0, 9]
+    c.reserve(16, 0)
+    c.advance()
+    assert c.pos.tolist() == [0, 10] and c.lens.tolist() == [1, 11]
+
+
+def test_the_length_counts_no_token_without_a_page():
+    c = PagedCache(1, 2, 64, 1, 64, 16, device="cpu")
+    c.reserve(3, 0)                            # one page; sequence 1 has none
+    for _ in range(20):
+        c.advance()
+    assert c.lens.tolist() == [16, 0] and c.pos.tolist() == [16, 0]
+    c.reserve(17)
+    c.advance()
+    assert c.pos.tolist() == [16, 0] and c.lens.tolist() == [17, 1]

@@ -207,3 +207,27 @@ def test_decoder_refusals():
         PagedCache(1, 1, 16, 1, 64, 24)
     with pytest.raises(ValueError):
         PagedCache(1, 1, 16, 1, 64, 16, dtype=torch.uint8)
+
+
+def test_decoder_reuses_a_place_while_others_go_on():
+    """A sequence that is released while the others go on, and given pages again later, attends to its own tokens alone:
+    its rows are a fresh stack's."""
+    p = params(7)
+    a, b = build(p, n_pages=T + 1), build(p)
+    codes = [torch.from_numpy(c.astype(np.int32)).cuda() for c in p["codes"]]
+    a.cache.reserve(16)
+    b.cache.reserve(16)
+    for i in range(5):
+        a.step(codes[i])
+    a.cache.release(0)
+    a.cache.reserve(17, 1)              # sequence 1 goes on in the page that sequence 0 had
+    for i in range(5, 11):
+        a.step(codes[i])
+    assert host(a.cache.lens).tolist() == [0, 11, 11]
+    zmoe_get_device_errors()
+    a.cache.release(1)
+    a.cache.reserve(16, 0)              # and gives it back, with its rows
+    for i in range(4):
+        x, y = a.step(codes[20 + i]), b.step(codes[20 + i])
+        assert_close(host(x)[:1], host(y)[:1].astype(np.float64), "bf16", f"h of the new sequence's step {i}")
+        assert host(a.cache.lens)[0] == i + 1
