@@ -42,7 +42,8 @@ class PagedCache:
 
     dtype torch.bfloat16, or torch.uint8 for E4M3 codes with k_scale, v_scale f32 [n_layers, Hkv].  Pages are handed
     out by ``reserve`` and taken back by ``release``; ``advance`` gives every sequence its next position.  ``lens`` counts
-    cached tokens only: it never passes ``room``, the tokens that a sequence's pages hold."""
+    cached tokens only: it never passes ``room``, the tokens that a sequence's pages hold.  A released sequence is idle
+    until it gets pages again: its tokens are padding (``seq`` -1), it stays at position 0 and counts no errors."""
 
     def __init__(self, n_layers: int, n_seqs: int, max_len: int, Hkv: int, D: int, page_size: int = 16,
                  n_pages: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
@@ -61,6 +62,7 @@ class PagedCache:
         self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=device)   # cached tokens
         self.pos = torch.zeros(n_seqs, dtype=torch.int32, device=device)    # the step's positions
         self.room = torch.zeros(n_seqs, dtype=torch.int32, device=device)   # tokens that the reserved pages hold
+        self.seq = torch.arange(n_seqs, dtype=torch.int32, device=device)   # the sequences' own numbers, -1: idle
         self.free: List[int] = list(range(self.n_pages - 1, -1, -1))
         self.pages: List[List[int]] = [[] for _ in range(n_seqs)]
 
@@ -79,14 +81,16 @@ class PagedCache:
             self.pages[s] += new
             self.table[s, have:need] = torch.tensor(new, dtype=torch.int32)
             self.room[s] = need * self.page_size
+            self.seq[s] = s
 
     def release(self, seq: int) -> None:
-        """Takes a sequence's pages back; it starts again at position 0."""
+        """Takes a sequence's pages back; it is idle until ``reserve`` gives it pages, and starts again at position 0."""
         self.free += reversed(self.pages[seq])
         self.pages[seq] = []
         self.table[seq].fill_(-1)
         self.lens[seq].zero_()
         self.room[seq].zero_()
+        self.seq[seq] = -1
 
     def advance(self, stream=None) -> None:
         """One more token for every sequence: its position in ``pos``, its new length in ``lens``.  A position
@@ -117,7 +121,7 @@ class AttentionRunner:
         self.q_in = qkv[:, :Hq * D].unflatten(1, (Hq, D))
         self.k_in = qkv[:, Hq * D:(Hq + Hkv) * D].unflatten(1, (Hkv, D))
         self.v_in = qkv[:, (Hq + Hkv) * D:].unflatten(1, (Hkv, D))
-        self.q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        self.q = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device=dev)   # a token that is not stored leaves its row
         self.gate = torch.empty((T, Hq), **f32)
         self.o = torch.empty((T, Hq, D), **f32)
         self.delta = torch.empty((T, d), **f32)
@@ -126,7 +130,8 @@ class AttentionRunner:
 
     def run(self, h: torch.Tensor, W: AttentionWeights, cache: PagedCache, layer: int, eps: float = 1e-6,
             gamma_next: Optional[torch.Tensor] = None, x_next: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """h <- h + the block's output for the token at cache.pos of each sequence, in place; h f32 [T, d].
+        """h <- h + the block's output for the token at cache.pos of each sequence, in place; h f32 [T, d].  An idle
+        sequence has no cached tokens, so its row of h stays.
 
         With ``gamma_next``, x_next [T, d] receives RMSNorm(h) * gamma_next of the new h (the next block's input)."""
         c = cache.layer(layer)
@@ -134,7 +139,7 @@ class AttentionRunner:
         Z.zmoe_speaker_prefix(self.x, W.w_qkv, out=self.qkv, stream=stream)
         if W.w_gate is not None:
             Z.zmoe_speaker_prefix(self.x, W.w_gate, out=self.gate, stream=stream)
-        Z.zmoe_kv_append(self.k_in, self.v_in, cache.pos, q=self.q_in, inv_freq=self.inv_freq,
+        Z.zmoe_kv_append(self.k_in, self.v_in, cache.pos, q=self.q_in, seq=cache.seq, inv_freq=self.inv_freq,
                          interleaved=self.interleaved, q_gamma=W.q_gamma, k_gamma=W.k_gamma, eps=eps, q_out=self.q,
                          stream=stream, **c)
         Z.zmoe_paged_attention(self.q, lens=cache.lens, gate=self.gate if W.w_gate is not None else None, out=self.o,

@@ -77,3 +77,15 @@ def test_the_length_counts_no_token_without_a_page():
     c.reserve(17)
     c.advance()
     assert c.pos.tolist() == [16, 0] and c.lens.tolist() == [17, 1]
+
+
+def test_a_released_sequence_is_padding_until_it_has_pages():
+    c = PagedCache(1, 3, 32, 1, 64, 16, device="cpu")
+    assert c.seq.tolist() == [0, 1, 2]         # without a page, but not released: its tokens count errors
+    c.reserve(1, 0)
+    c.release(1)
+    c.release(0)
+    assert c.seq.tolist() == [-1, -1, 2]
+    c.reserve(0, 1)                            # no pages, so idle as before
+    c.reserve(17, 0)
+    assert c.seq.tolist() == [0, -1, 2] and c.room.tolist() == [32, 0, 0]

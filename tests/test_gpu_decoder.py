@@ -231,3 +231,30 @@ def test_decoder_reuses_a_place_while_others_go_on():
         x, y = a.step(codes[20 + i]), b.step(codes[20 + i])
         assert_close(host(x)[:1], host(y)[:1].astype(np.float64), "bf16", f"h of the new sequence's step {i}")
         assert host(a.cache.lens)[0] == i + 1
+
+
+def test_decoder_with_idle_places():
+    """Released sequences are padding: they count no errors, the attention leaves their rows, and the others' rows are
+    what they are without them."""
+    p = params(8)
+    a, b = build(p), build(p)
+    codes = [torch.from_numpy(c.astype(np.int32)).cuda() for c in p["codes"]]
+    for st in (a, b):
+        st.cache.reserve(24)
+        st.step(codes[0])
+    b.cache.release(0)
+    b.cache.release(2)
+    pages = b.cache.k.clone(), b.cache.v.clone()
+    for i in range(1, 20):
+        x, y = a.step(codes[i]), b.step(codes[i])
+        assert_close(host(y)[1:2], host(x)[1:2].astype(np.float64), "bf16", f"h of step {i}")
+    assert zmoe_get_device_errors() == 0
+    assert host(b.cache.lens).tolist() == [0, 20, 0]
+    mine = b.cache.pages[1]
+    others = [i for i in range(b.cache.n_pages) if i not in mine]
+    assert torch.equal(b.cache.k[:, others], pages[0][:, others]) and torch.equal(b.cache.v[:, others], pages[1][:, others])
+    A, run = b.attention[0], b.att_runners[HQ, HKV, D]
+    h = torch.randn((T, D_MODEL), device="cuda")
+    got = run.run(h.clone(), A, b.cache, 0)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], h[0]) and torch.equal(got[2], h[2]) and not torch.equal(got[1], h[1])
