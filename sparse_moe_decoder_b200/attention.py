@@ -43,7 +43,8 @@ class PagedCache:
     dtype torch.bfloat16, or torch.uint8 for E4M3 codes with k_scale, v_scale f32 [n_layers, Hkv].  Pages are handed
     out by ``reserve`` and taken back by ``release``; ``advance`` gives every sequence its next position.  ``lens`` counts
     cached tokens only: it never passes ``room``, the tokens that a sequence's pages hold.  A released sequence is idle
-    until it gets pages again: its tokens are padding (``seq`` -1), it stays at position 0 and counts no errors."""
+    until it gets pages again: its tokens are padding (``seq`` -1), it stays at position 0 and counts no errors.  A place
+    that has had no sequence yet is made idle in the same way."""
 
     def __init__(self, n_layers: int, n_seqs: int, max_len: int, Hkv: int, D: int, page_size: int = 16,
                  n_pages: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
@@ -63,6 +64,8 @@ class PagedCache:
         self.pos = torch.zeros(n_seqs, dtype=torch.int32, device=device)    # the step's positions
         self.room = torch.zeros(n_seqs, dtype=torch.int32, device=device)   # tokens that the reserved pages hold
         self.seq = torch.arange(n_seqs, dtype=torch.int32, device=device)   # the sequences' own numbers, -1: idle
+        self.idle = torch.zeros(n_seqs, dtype=torch.int32, device=device)   # -1 where idle, 0 elsewhere
+        self.rules: List["LogitRules"] = []   # whose streams these sequences are: they forget a sequence with its release
         self.free: List[int] = list(range(self.n_pages - 1, -1, -1))
         self.pages: List[List[int]] = [[] for _ in range(n_seqs)]
 
@@ -82,15 +85,20 @@ class PagedCache:
             self.table[s, have:need] = torch.tensor(new, dtype=torch.int32)
             self.room[s] = need * self.page_size
             self.seq[s] = s
+            self.idle[s] = 0
 
     def release(self, seq: int) -> None:
-        """Takes a sequence's pages back; it is idle until ``reserve`` gives it pages, and starts again at position 0."""
+        """Takes a sequence's pages back; it is idle until ``reserve`` gives it pages, and starts again at position 0,
+        with no frames in the history of ``rules``."""
         self.free += reversed(self.pages[seq])
         self.pages[seq] = []
         self.table[seq].fill_(-1)
         self.lens[seq].zero_()
         self.room[seq].zero_()
         self.seq[seq] = -1
+        self.idle[seq] = -1
+        for r in self.rules:
+            r.release(seq)
 
     def advance(self, stream=None) -> None:
         """One more token for every sequence: its position in ``pos``, its new length in ``lens``.  A position
@@ -164,17 +172,25 @@ class LogitRules:
         self.repetition, self.presence, self.frequency, self.bias, self.mask = repetition, presence, frequency, bias, mask
         self.history = torch.full((T, window, N), -1, dtype=torch.int32, device=device)
         self.hist_lens = torch.zeros(T, dtype=torch.int32, device=device)
-        self.slot = torch.zeros(1, dtype=torch.int64, device=device)   # where the next frame goes; the order is free
+        self.frame = torch.empty((T, N), dtype=torch.int32, device=device)
+        # where the next frame of every stream goes: the order is free, and -1 is no id
+        self.slot = torch.zeros(1, dtype=torch.int64, device=device)
 
     def choose(self, logits: torch.Tensor, ids: torch.Tensor, stream=None) -> None:
         """Adjusts logits [T, N, V] in place and writes the greedy frame to ids int32 [T, N]."""
         Z.zmoe_adjust_logits(logits, self.history, self.hist_lens, self.repetition, self.presence, self.frequency,
                              self.bias, self.mask, out=logits, ids=ids, stream=stream)
 
-    def remember(self, ids: torch.Tensor, stream=None) -> None:
-        """Adds the frame ids [T, N] to the history, in place of the oldest when the window is full."""
+    def release(self, stream_index: int) -> None:
+        """Forgets the frames of one stream, for the next request in its place."""
+        self.history[stream_index].fill_(-1)
+
+    def remember(self, ids: torch.Tensor, stream=None, idle: Optional[torch.Tensor] = None) -> None:
+        """Adds the frame ids [T, N] to the history, in place of the oldest when the window is full.  Of streams whose
+        entry in idle int32 [T] is -1 (of the others it is 0) nothing is added."""
         window = self.history.shape[1]
         with torch.cuda.stream(stream):
-            self.history.index_copy_(1, self.slot, ids.unsqueeze(1))
+            frame = ids if idle is None else torch.bitwise_or(ids, idle.unsqueeze(1), out=self.frame)   # -1 where idle
+            self.history.index_copy_(1, self.slot, frame.unsqueeze(1))
             self.slot.add_(1).remainder_(window)
             self.hist_lens.add_(1).clamp_(max=window)

@@ -162,7 +162,7 @@ class DecodeStack:
     each layer is the decoder's: the attention block, then the MoE layer; every step adds a token to each sequence
     (``cache.reserve`` gives out the pages).  inv_freq f64 [rotary_dim / 2] and ``interleaved``: zmoe_kv_append's.
     With ``rules`` the heads' logits (kept in ``logits``) are adjusted before the next frame is chosen, and the frame
-    joins the rules' history."""
+    joins the rules' history.  ``release`` frees a sequence's place for another one."""
 
     def __init__(self, tables: torch.Tensor, gamma0: torch.Tensor, layers: List[MoEWeights], eps: float = 1e-6,
                  T: int = 1, w_heads: Optional[torch.Tensor] = None, gamma_out: Optional[torch.Tensor] = None,
@@ -192,6 +192,10 @@ class DecodeStack:
             persistent = False
         if rules is not None and w_heads is None:
             raise ValueError("rules need the heads")
+        if rules is not None and rules.history.shape[0] != T:
+            raise ValueError("rules of as many streams as the step has tokens")
+        if rules is not None and attention is not None and rules not in cache.rules:
+            cache.rules.append(rules)
         self.attention, self.cache, self.rules = attention, cache, rules
         self.att_runners = {}
         for A in attention or []:
@@ -267,7 +271,15 @@ class DecodeStack:
                                 stream=stream)
             if self.rules is not None:
                 self.rules.choose(self.logits, self.next_ids, stream)
-                self.rules.remember(self.next_ids, stream)
+                self.rules.remember(self.next_ids, stream, self.cache.idle if self.attention is not None else None)
+
+    def release(self, seq: int) -> None:
+        """Ends a sequence: its pages go back (it is idle until ``cache.reserve`` gives it pages) and the rules forget
+        its frames.  Without a cache the next step starts the next sequence in its place."""
+        if self.attention is not None:
+            self.cache.release(seq)         # which tells the rules
+        elif self.rules is not None:
+            self.rules.release(seq)
 
 
 def stack_from_bits(tables_bits, gamma0, layer_small, expert_bits, n_layers: int, E: int, d: int, f: int,

@@ -89,3 +89,24 @@ def test_a_released_sequence_is_padding_until_it_has_pages():
     c.reserve(0, 1)                            # no pages, so idle as before
     c.reserve(17, 0)
     assert c.seq.tolist() == [0, -1, 2] and c.room.tolist() == [32, 0, 0]
+
+
+def test_a_released_stream_forgets_its_frames():
+    c, r = PagedCache(1, 2, 64, 1, 64, 16, device="cpu"), LogitRules(2, 2, 8, device="cpu")
+    c.rules.append(r)
+    c.reserve(64)
+    for i in range(5):
+        c.advance()
+        r.remember(torch.full((2, 2), i, dtype=torch.int32), idle=c.idle)
+    c.release(0)
+    kept = lambda t: sorted(x for x in r.history[t, :r.hist_lens[t], 0].tolist() if x >= 0)  # noqa: E731
+    assert kept(0) == [] and kept(1) == [0, 1, 2, 3, 4]
+    for i in range(5, 7):                      # nothing is added while it is idle
+        c.advance()
+        r.remember(torch.full((2, 2), i, dtype=torch.int32), idle=c.idle)
+    c.reserve(16, 0)
+    assert kept(0) == [] and kept(1) == [0, 1, 2, 3, 4, 5, 6]
+    for i in range(7, 19):                     # from here on the window of the one before it
+        c.advance()
+        r.remember(torch.full((2, 2), i, dtype=torch.int32), idle=c.idle)
+        assert kept(0) == list(range(max(7, i - 7), i + 1)) and kept(1) == list(range(max(0, i - 7), i + 1))

@@ -258,3 +258,51 @@ def test_decoder_with_idle_places():
     got = run.run(h.clone(), A, b.cache, 0)
     torch.cuda.synchronize()
     assert torch.equal(got[0], h[0]) and torch.equal(got[2], h[2]) and not torch.equal(got[1], h[1])
+
+
+def test_decoder_forgets_the_frames_of_a_released_sequence():
+    """Logits and ids of a place that is used again are a fresh stack's, though the other sequences go on and idle
+    steps lie between."""
+    p = params(9)
+    p["rep"][:] = 4.0                   # a penalty that shows
+    a, b = build(p), build(p)
+    codes = [torch.from_numpy(c.astype(np.int32)).cuda() for c in p["codes"]]
+    a.cache.reserve(40)
+    b.cache.reserve(40)
+    for i in range(7):
+        a.step(codes[i])
+    a.release(0)
+    for i in range(7, 10):
+        a.step(codes[i])
+    a.cache.reserve(40, 0)
+    for i in range(12):
+        a.step(codes[20 + i])
+        b.step(codes[20 + i])
+        ok = p["ok"][:1]
+        x, y = host(a.logits)[:1].astype(np.float64), host(b.logits)[:1].astype(np.float64)
+        assert_close(np.where(ok, x, 0), np.where(ok, y, 0), "bf16", f"logits of the new sequence's step {i}")
+        assert np.array_equal(host(a.next_ids)[0], oracle.allowed_greedy(host(a.logits)[:1], ok)[0])
+        # the two may choose otherwise only between logits that are as near as the bar
+        if not np.array_equal(host(a.next_ids)[0], host(b.next_ids)[0]):
+            break
+    assert i >= 5
+    assert zmoe_get_device_errors() == 0
+
+
+def test_rules_of_another_count_are_refused():
+    p = params(6)
+    st = build(p)
+    with pytest.raises(ValueError, match="streams"):
+        DecodeStack(st.tables, st.gamma0, st.layers, T=T, w_heads=st.w_heads, gamma_out=st.gamma_out,
+                    rules=LogitRules(T + 1, N, WINDOW))
+
+
+def test_release_without_a_cache():
+    p = params(6)
+    st = build(p)
+    st = DecodeStack(st.tables, st.gamma0, st.layers, T=T, w_heads=st.w_heads, gamma_out=st.gamma_out,
+                     rules=LogitRules(T, N, WINDOW, torch.full((T,), 2.0, device="cuda")))
+    for i in range(3):
+        st.step(torch.from_numpy(p["codes"][i].astype(np.int32)).cuda())
+    st.release(1)
+    assert host((st.rules.history >= 0).sum((1, 2))).tolist() == [3 * N, 0, 3 * N]
