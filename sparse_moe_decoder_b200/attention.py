@@ -69,8 +69,9 @@ class PagedCache:
         self.free: List[int] = list(range(self.n_pages - 1, -1, -1))
         self.pages: List[List[int]] = [[] for _ in range(n_seqs)]
 
-    def reserve(self, length: int, seq: Optional[int] = None) -> None:
-        """Pages for the first ``length`` tokens of sequence ``seq`` (None: of every sequence)."""
+    def reserve(self, length: int, seq: Optional[int] = None, stream=None) -> None:
+        """Pages for the first ``length`` tokens of sequence ``seq`` (None: of every sequence).  The device's side of it
+        happens on ``stream`` (None: the current one): the stream of the steps, between which it belongs."""
         if length > self.max_len:
             raise ValueError(f"{length} tokens in a cache of {self.max_len}")
         need = -(-length // self.page_size)
@@ -82,23 +83,25 @@ class PagedCache:
                 raise RuntimeError(f"the cache is out of pages: sequence {s} needs {need - have}, {len(self.free)} are free")
             new = [self.free.pop() for _ in range(need - have)]
             self.pages[s] += new
-            self.table[s, have:need] = torch.tensor(new, dtype=torch.int32)
-            self.room[s] = need * self.page_size
-            self.seq[s] = s
-            self.idle[s] = 0
+            with torch.cuda.stream(stream):
+                self.table[s, have:need] = torch.tensor(new, dtype=torch.int32)
+                self.room[s] = need * self.page_size
+                self.seq[s] = s
+                self.idle[s] = 0
 
-    def release(self, seq: int) -> None:
+    def release(self, seq: int, stream=None) -> None:
         """Takes a sequence's pages back; it is idle until ``reserve`` gives it pages, and starts again at position 0,
-        with no frames in the history of ``rules``."""
+        with no frames in the history of ``rules``.  ``stream``: as for ``reserve``."""
         self.free += reversed(self.pages[seq])
         self.pages[seq] = []
-        self.table[seq].fill_(-1)
-        self.lens[seq].zero_()
-        self.room[seq].zero_()
-        self.seq[seq] = -1
-        self.idle[seq] = -1
+        with torch.cuda.stream(stream):
+            self.table[seq].fill_(-1)
+            self.lens[seq].zero_()
+            self.room[seq].zero_()
+            self.seq[seq] = -1
+            self.idle[seq] = -1
         for r in self.rules:
-            r.release(seq)
+            r.release(seq, stream)
 
     def advance(self, stream=None) -> None:
         """One more token for every sequence: its position in ``pos``, its new length in ``lens``.  A position
@@ -181,9 +184,10 @@ class LogitRules:
         Z.zmoe_adjust_logits(logits, self.history, self.hist_lens, self.repetition, self.presence, self.frequency,
                              self.bias, self.mask, out=logits, ids=ids, stream=stream)
 
-    def release(self, stream_index: int) -> None:
-        """Forgets the frames of one stream, for the next request in its place."""
-        self.history[stream_index].fill_(-1)
+    def release(self, t: int, stream=None) -> None:
+        """Forgets the frames of stream ``t`` of the T, for the next request in its place."""
+        with torch.cuda.stream(stream):
+            self.history[t].fill_(-1)
 
     def remember(self, ids: torch.Tensor, stream=None, idle: Optional[torch.Tensor] = None) -> None:
         """Adds the frame ids [T, N] to the history, in place of the oldest when the window is full.  Of streams whose

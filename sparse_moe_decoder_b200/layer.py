@@ -273,13 +273,13 @@ class DecodeStack:
                 self.rules.choose(self.logits, self.next_ids, stream)
                 self.rules.remember(self.next_ids, stream, self.cache.idle if self.attention is not None else None)
 
-    def release(self, seq: int) -> None:
+    def release(self, seq: int, stream=None) -> None:
         """Ends a sequence: its pages go back (it is idle until ``cache.reserve`` gives it pages) and the rules forget
-        its frames.  Without a cache the next step starts the next sequence in its place."""
+        its frames.  Without a cache the next step starts the next sequence in its place.  ``stream``: that of the steps."""
         if self.attention is not None:
-            self.cache.release(seq)         # which tells the rules
+            self.cache.release(seq, stream)         # which tells the rules
         elif self.rules is not None:
-            self.rules.release(seq)
+            self.rules.release(seq, stream)
 
 
 def stack_from_bits(tables_bits, gamma0, layer_small, expert_bits, n_layers: int, E: int, d: int, f: int,

@@ -306,3 +306,33 @@ def test_release_without_a_cache():
         st.step(torch.from_numpy(p["codes"][i].astype(np.int32)).cuda())
     st.release(1)
     assert host((st.rules.history >= 0).sum((1, 2))).tolist() == [3 * N, 0, 3 * N]
+
+
+def test_decoder_releases_between_steps_of_another_stream():
+    """Steps, releases and pages on a side stream that lags behind the host, with no wait between them."""
+    p = params(10)
+    codes = [torch.from_numpy(c.astype(np.int32)).cuda() for c in p["codes"]]
+    side = torch.cuda.Stream()
+
+    def run(stream, lag):
+        st, out = build(p, n_pages=T + 1), []
+        st.cache.reserve(16)
+        torch.cuda.synchronize()
+        for i in range(12):
+            if lag:
+                with torch.cuda.stream(stream):
+                    torch.cuda._sleep(20_000_000)
+            if i in (4, 8):
+                st.release(i % 3, stream=stream)
+                st.cache.reserve(16, i % 3, stream=stream)
+            with torch.cuda.stream(stream):
+                st.ids.copy_(codes[i])
+            st.step(stream=stream)
+            with torch.cuda.stream(stream):
+                out += [st.h.clone(), st.logits.clone(), st.next_ids.clone(), st.cache.lens.clone()]
+        torch.cuda.synchronize()
+        return out
+
+    want, got = run(None, False), run(side, True)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert host(got[-1]).tolist() == [12, 8, 4] and zmoe_get_device_errors() == 0
