@@ -222,7 +222,12 @@ class DecodeStack:
                             layer_x=torch.empty((nL, d), dtype=L0.dtype, device=dev))
 
     def step(self, ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """One decode step; returns the final fp32 residual stream h [T, d]."""
+        """One decode step; returns the final fp32 residual stream h [T, d].  All of it happens on ``stream`` (None: the
+        current one), the copy of ``ids`` too."""
+        with torch.cuda.stream(stream):
+            return self._step(ids, stream)
+
+    def _step(self, ids: Optional[torch.Tensor], stream) -> torch.Tensor:
         if ids is not None:
             self.ids.copy_(ids)
         if self.persistent:

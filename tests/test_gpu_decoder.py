@@ -336,3 +336,28 @@ def test_decoder_releases_between_steps_of_another_stream():
     want, got = run(None, False), run(side, True)
     assert all(torch.equal(x, y) for x, y in zip(want, got))
     assert host(got[-1]).tolist() == [12, 8, 4] and zmoe_get_device_errors() == 0
+
+
+def test_decoder_takes_its_ids_on_the_stream_of_the_step():
+    """A step's ids are copied behind the steps before it, also where these lag behind the host."""
+    p = params(11)
+    codes = [torch.from_numpy(c.astype(np.int32)).cuda() for c in p["codes"]]
+    side = torch.cuda.Stream()
+
+    def run(stream, lag):
+        st, out = build(p), []
+        st.cache.reserve(16)
+        st.record_inputs = True
+        torch.cuda.synchronize()
+        if lag:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(200_000_000)
+        for i in range(6):
+            st.step(codes[i], stream=stream)
+            with torch.cuda.stream(stream):
+                out += [st.h.clone(), st.next_ids.clone()] + st.layer_inputs + st.layer_h + st.layer_idx
+        torch.cuda.synchronize()
+        return out
+
+    want, got = run(None, False), run(side, True)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
