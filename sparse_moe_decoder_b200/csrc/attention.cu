@@ -730,11 +730,11 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, HT>::warps, 1)
     for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
     for (uint32_t left = mine_of; left;) {   // four parts at a time
       float v[4][kCols], k[4];
+      const int here = __popc(left) < 4 ? __popc(left) : 4;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int i = left ? __ffs(left) - 1 : first;
         k[q] = __shfl_sync(0xffffffffu, weight, i);
-        if (!left) k[q] = 0.f;
         left &= left - 1;
         const float* p = segments[i].part + 2 * H + head * D + kCols * lane;
         if (kCols == 4) {
@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, HT>::warps, 1)
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
-          if (k[q] != 0.f) acc[c] = fmaf(v[q][c], k[q], acc[c]);   // an empty part's zeros meet no infinity
+          if (q < here) acc[c] = fmaf(v[q][c], k[q], acc[c]);   // a part of weight 0 counts: its NaN stays one
     }
     const Segment& seg = segments[first];
     const int hk = seg.u / a.gtiles, hd = (seg.u - hk * a.gtiles) * H + head;

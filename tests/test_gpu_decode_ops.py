@@ -961,3 +961,32 @@ def test_logits_of_long_rows_with_masks_and_no_bias():
     ok[:100, 0, V - 1] = True
     ok[100:200, 0, 1] = True
     assert torch.equal(out, torch.where(ok, z, float("-inf")))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,n,top", [(1, 33, 32), (1, 600, 599), (1, 600, 100), (1, 20000, 100), (1, 20000, 19999), (40, 1000, 100)])
+@pytest.mark.parametrize("Hq", [8, 16])
+def test_attention_nan_far_below_the_largest_score(B, n, top, Hq, kv):
+    """exp(score) underflows to 0 where the value is NaN, and 0 x NaN is NaN: in its column of its sequence's heads, however
+    the cache is cut (600 tokens: parts that the second kernel joins; 20000: a CTA joins those of its 192 tokens first)."""
+    D, page = 64, 16
+    cols = -(-n // page)
+    r = rnd(n)
+    table = r.permutation(B * cols).reshape(B, cols).astype(np.int32)
+    k = np.zeros((B * cols, 1, page, D), np.float32)
+    v = r.integers(-8, 9, (B * cols, 1, page, D)).astype(np.float32)
+    best = table[:, top // page], 0, top % page
+    k[best + (0,)] = 16.0                                                # a score of 256, and of 0 elsewhere
+    v[table[:, 0], 0, 5, 3] = np.nan
+    if kv == "e4m3":
+        kc, vc = (torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).cuda() for x in (k, v))
+        sc = torch.ones(1, device="cuda")
+    else:
+        kc, vc, sc = dev(k, BF16), dev(v, BF16), None
+    q = torch.zeros((B, Hq, D), dtype=BF16, device="cuda")
+    q[:, :, 0] = 16.0
+    out = zmoe_paged_attention(q, kc, vc, dev(table), torch.full((B,), n, dtype=torch.int32, device="cuda"), scale=1.0,
+                               k_scale=sc, v_scale=sc)
+    want = np.repeat(v[best][:, None], Hq, 1)                            # all the weight lies on that token
+    want[:, :, 3] = np.nan
+    assert np.array_equal(f64(out), want, equal_nan=True)
