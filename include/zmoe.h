@@ -444,7 +444,9 @@ ZMOE_API zmoe_status zmoe_decode_stack(const zmoe_stack_layer* layers, int n_lay
  *           where every x is 0
  *   codes[t, c] = the E4M3 value nearest x[t, c] * fp32(1 / scale) (ties to even, saturating at 448)
  * The codes take the fp32 x, before its rounding to x_dtype.  A row that holds a NaN has NaN codes (0x7F) and
- * scale 1; an infinite h' gives NaN in its own column and 0 elsewhere, as the formula does.
+ * scale 1; an infinite h' gives NaN in its own column and 0 elsewhere, as the formula does.  The squares are summed in
+ * fp32: a finite row whose sum of squares reaches 2^128 gives 0 as well, and with eps below 2^-126 a row's largest
+ * magnitude has to be 2^-56 or more (a row of zeros without eps is 0 / 0: NaN).
  *   h, h_out: [T, d] of h_dtype; delta: [T, d] of delta_dtype or NULL; gamma: f32 [d]; x: [T, d] of x_dtype;
  *   codes: uint8 [T, d]; scales: f32 [T] (group 0) or [T, d / 128].  h_out, x and (codes with scales) are optional
  *   (NULL), at least one is given.  h_out may be h or delta (of the same type).
@@ -459,7 +461,8 @@ ZMOE_API zmoe_status zmoe_add_rmsnorm(const void* h, zmoe_dtype h_dtype, const v
  * Appends keys and values to a paged cache, queries and keys normed and rotated by position on the way
  * ([DIGEST] item 5: grouped-query attention with rotary positions; "Builds on" lists the rotary embedding and
  * query/key norms).  Token t is at position p = pos[t] of sequence s = seq[t] (seq NULL: s = t).  Per head:
- *   y = x / sqrt(mean_c x_c^2 + eps) * gamma                  (queries with q_gamma, keys with k_gamma; NULL: y = x)
+ *   y = x / sqrt(mean_c x_c^2 + eps) * gamma                  (queries with q_gamma, keys with k_gamma; NULL: y = x;
+ *                                                              the range of x is zmoe_add_rmsnorm's of h')
  *   the first rotary_dim columns of queries and keys are turned pair by pair by w = p * inv_freq[i]:
  *     (y_a, y_b) <- (y_a cos w - y_b sin w, y_a sin w + y_b cos w)
  *     with (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved != 0

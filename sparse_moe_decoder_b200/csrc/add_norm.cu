@@ -6,7 +6,8 @@
 //   x[t]  = h'[t] / sqrt(mean_c h'[t, c]^2 + eps) * gamma       (of the rounded h', in fp32)
 //   s     = max|x| / 448 over a row, or over each 128 columns;  codes = E4M3 nearest x * fp32(1 / s)
 // The codes take the unrounded fp32 x, so that they carry one rounding; x itself is rounded to its type
-// once, on its way out.
+// once, on its way out.  The squares are summed in fp32 as they are: no row of a trained model comes near 2^64 or, without
+// eps, 2^-56, and scaling such rows first cost 1 to 6% of every other row's time (a second sum behind a branch).
 //
 // Bound by HBM: h and delta are read once, h', x and the codes written once.  A row stays in its threads'
 // registers between the two reductions (sum of squares, largest magnitude).  A thread takes chunks of CH

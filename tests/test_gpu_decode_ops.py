@@ -990,3 +990,34 @@ def test_attention_nan_far_below_the_largest_score(B, n, top, Hq, kv):
     want = np.repeat(v[best][:, None], Hq, 1)                            # all the weight lies on that token
     want[:, :, 3] = np.nan
     assert np.array_equal(f64(out), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("types", ["f32 f32 bf16", "bf16 bf16 f32", "f32 bf16 f32", "bf16 f32 bf16"])
+@pytest.mark.parametrize("T,d", [(40, 24), (9, 256), (5, 2048), (4, 8192), (4, 32768), (2500, 384)])
+def test_norm_rows_at_the_ends_of_the_range(T, d, types):
+    """eps 0 scales a row to one, from a largest magnitude of 2^-56 to a sum of squares of 2^127: the squares below 2^-149
+    that fp32 loses are d 2^-150 together, 2^-23 of the largest one's 2^-112."""
+    ht, dt, xt = (F32 if n == "f32" else BF16 for n in types.split())
+    r = rnd(d)
+    h = r.uniform(-1, 1, (T, d))
+    h[:, 5] = 1.0
+    size = np.array([2.0 ** -56, 1e-12, 1.0, 2.0 ** 63 / np.sqrt(d)])[np.arange(T) % 4]
+    h, gamma = dev(h * size[:, None], ht), dev(1 + 0.2 * r.standard_normal(d), F32)
+    delta = dev(r.uniform(0, 0.01, (T, d)) * size[:, None], dt)
+    for group in (0, 128) if d % 128 == 0 else (0,):
+        o = zmoe_add_rmsnorm(h, gamma, delta, 0.0, out_dtype=xt, want_codes=True, group=group)
+        check_norm(o, h, delta, gamma, 0.0, xt, group)
+    # an eps of 2^-126 or more leaves no lower end: rows of subnormal numbers go to 0 as the formula has them
+    eps = 2.0 ** -126
+    tiny = dev(r.standard_normal((T, d)) * 1e-39, F32)
+    check_norm(zmoe_add_rmsnorm(tiny, gamma, None, eps, out_dtype=xt), tiny, None, gamma, eps, xt, 0)
+
+
+def test_norm_beyond_the_range():
+    """Documented: a finite row whose sum of squares passes fp32's range gives 0, codes of 0 and scale 1; without eps a row
+    of zeros gives NaN."""
+    h = torch.full((2, 256), 1e30, device="cuda")
+    h[1] = 0
+    o = zmoe_add_rmsnorm(h, torch.ones(256, device="cuda"), eps=0.0, out_dtype=F32, want_codes=True)
+    assert not o["x"][0].any() and not o["codes"][0].any() and o["scales"][0].item() == 1
+    assert bool(torch.isnan(o["x"][1]).all()) and bool((o["codes"][1] & 0x7F == NAN_CODE).all())
