@@ -1021,3 +1021,66 @@ def test_norm_beyond_the_range():
     o = zmoe_add_rmsnorm(h, torch.ones(256, device="cuda"), eps=0.0, out_dtype=F32, want_codes=True)
     assert not o["x"][0].any() and not o["codes"][0].any() and o["scales"][0].item() == 1
     assert bool(torch.isnan(o["x"][1]).all()) and bool((o["codes"][1] & 0x7F == NAN_CODE).all())
+
+
+def chained_state():
+    r = rnd(61)
+    kc, vc, _, _ = make_cache(r, 60, 2, 16, 64, "bf16")
+    f = lambda *s: dev(r.standard_normal(s), F32)  # noqa: E731
+    pos = dev(np.array([40, 0, 310], np.int32))
+    return dict(kc=kc, vc=vc, table=dev(r.permutation(60).reshape(3, 20).astype(np.int32)), pos=pos, lens=pos + 1, h=f(3, 512),
+                delta=f(3, 512), gamma=1 + 0.1 * f(512), ones=torch.ones(512, device="cuda"), xkv=f(3, 512), xq=f(3, 512),
+                q=torch.empty((3, 8, 64), dtype=BF16, device="cuda"), o=torch.empty((3, 8, 64), device="cuda"),
+                bias=f(1, 512), rep=torch.full((3,), 1.3, device="cuda"), frq=torch.full((3,), 0.2, device="cuda"),
+                ids=[torch.zeros((3, 1), dtype=torch.int32, device="cuda") for _ in range(2)],
+                inv=dev(10000.0 ** (-np.arange(0, 64, 2) / 64)),
+                ws=torch.empty(zmoe_paged_attention_workspace_size(3, 8, 2, 64), dtype=torch.uint8, device="cuda"))
+
+
+def chained_step(s, i, after=lambda: None):
+    """Every input that changes is the output of the operator before it or of the step before: the keys and values are the
+    norm's, the queries the norm of the attention's output, the residual that output's adjusted values, the history the
+    ids of the step before."""
+    kv = s["xkv"].view(3, 8, 64)
+    zmoe_add_rmsnorm(s["h"], s["gamma"], s["delta"], outs=dict(h=s["h"], x=s["xkv"]))
+    after()
+    zmoe_kv_append(kv[:, :2], kv[:, 2:4], s["pos"], s["kc"], s["vc"], s["table"], q=s["xq"].view(3, 8, 64), inv_freq=s["inv"],
+                   q_out=s["q"])
+    after()
+    zmoe_paged_attention(s["q"], s["kc"], s["vc"], s["table"], s["lens"], out=s["o"], workspace=s["ws"])
+    after()
+    zmoe_add_rmsnorm(s["o"].view(3, 512), s["ones"], outs=dict(x=s["xq"]))
+    after()
+    zmoe_adjust_logits(s["o"].view(3, 1, 512), s["ids"][i % 2].view(3, 1, 1), repetition=s["rep"], frequency=s["frq"],
+                       bias=s["bias"], out=s["delta"].view(3, 1, 512), ids=s["ids"][1 - i % 2])
+    after()
+
+
+def test_chains_through_every_operator():
+    """Sixty dependent steps, each kernel launched beside the one whose output it reads: as with a wait between all calls,
+    and as two steps captured and replayed."""
+    names = ("h", "delta", "xkv", "xq", "q", "o", "kc", "vc")
+
+    def run(after):
+        s = chained_state()
+        torch.cuda.synchronize()
+        for i in range(60):
+            chained_step(s, i, after)
+        torch.cuda.synchronize()
+        return [s[k] for k in names] + s["ids"]
+
+    want = run(torch.cuda.synchronize)
+    assert all(bool(torch.isfinite(t.float()).all()) for t in want)
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(want, run(lambda: None)))
+    s = chained_state()
+    chained_step(chained_state(), 0)                                     # first use outside the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chained_step(s, 0)
+        chained_step(s, 1)
+    for _ in range(30):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, [s[k] for k in names] + s["ids"]))
