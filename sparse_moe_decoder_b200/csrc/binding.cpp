@@ -305,6 +305,8 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int64_t L = 0;
     if (a[1] != Py_None) L = contiguous(a[1], "history", 3).size(1);
     const void* hist = address(a[1], "history", dev, {T, L, N}, at::kInt);
+    static const int32_t no_frames = 0;   // a history of no frames has no address, and is none the less one; never read
+    if (a[1] != Py_None && L == 0) hist = &no_frames;
     const void* lens = address(a[2], "hist_lens", dev, {T}, at::kInt);
     const void* rep = address(a[3], "repetition", dev, {T}, at::kFloat);
     const void* pre = address(a[4], "presence", dev, {T}, at::kFloat);

@@ -1084,3 +1084,16 @@ def test_chains_through_every_operator():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want, [s[k] for k in names] + s["ids"]))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_logits_with_a_history_of_no_frames(dtype):
+    """The first step of a stream: nothing is penalised yet."""
+    z = dev(rnd(71).standard_normal((2, 3, 77)), dtype)
+    one = torch.ones(2, device="cuda")
+    hist, lens = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((2, 0, 3), (2,)))
+    for kw in (dict(repetition=2 * one), dict(presence=one, frequency=one), dict(hist_lens=lens, repetition=2 * one)):
+        out, ids = zmoe_adjust_logits(z, hist, **kw)
+        assert torch.equal(out, z) and torch.equal(ids.long(), z.float().argmax(2))
+    with pytest.raises(Exception, match="penalties need a history"):
+        zmoe_adjust_logits(z, repetition=one)
