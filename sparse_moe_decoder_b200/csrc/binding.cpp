@@ -102,6 +102,15 @@ float real(PyObject* o, const char* name) {
   return static_cast<float>(v);
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    bad(PyExc_TypeError, name, " must be true or false");
+  }
+  return v == 1;
+}
+
 int size32(int64_t v, const char* name) {
   if (v > INT32_MAX) bad(PyExc_ValueError, name, " does not fit 32 bits");
   return static_cast<int>(v);
@@ -258,7 +267,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* kg = address(a[11], "k_gamma", c.dev, {c.D}, at::kFloat);
     const Place at(c.dev, a[16]);
     return zmoe_kv_append(qh.p, kh.p, vh.p, type, qh.stride, kh.stride, vh.stride, static_cast<const int32_t*>(seq),
-                          static_cast<const int32_t*>(pos), static_cast<const double*>(freq), rot, PyObject_IsTrue(a[9]) == 1,
+                          static_cast<const int32_t*>(pos), static_cast<const double*>(freq), rot, truth(a[9], "interleaved"),
                           static_cast<const float*>(qg), static_cast<const float*>(kg), real(a[12], "eps"), size32(T, "T"),
                           size32(Hq, "Hq"), size32(c.Hkv, "Hkv"), size32(c.D, "D"), q_out, c.k, c.v, c.type, c.k_scale,
                           c.v_scale, table.p, table.rows, table.cols, size32(c.n_pages, "n_pages"),

@@ -1097,3 +1097,13 @@ def test_logits_with_a_history_of_no_frames(dtype):
         assert torch.equal(out, z) and torch.equal(ids.long(), z.float().argmax(2))
     with pytest.raises(Exception, match="penalties need a history"):
         zmoe_adjust_logits(z, repetition=one)
+
+
+def test_append_refuses_what_is_neither_true_nor_false():
+    kc, vc, _, _ = make_cache(rnd(0), 4, 2, 16, 64, "bf16")
+    before = kc.clone(), vc.clone()
+    kv = torch.ones((2, 2, 64), dtype=BF16, device="cuda")
+    pos, table = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError, match="interleaved must be true or false"):
+        zmoe_kv_append(kv, kv, pos, kc, vc, table, interleaved=torch.ones(2))
+    assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
