@@ -125,6 +125,9 @@ class AttentionRunner:
     def __init__(self, T: int, d: int, Hq: int, Hkv: int, D: int, inv_freq: Optional[torch.Tensor] = None,
                  interleaved: bool = False, device="cuda"):
         dev = torch.device(device)
+        if D not in (64, 128) or d < 8 or d % 8 or max(d, Hq * D) > 6400:
+            raise ValueError(f"heads of 64 or 128 columns, d a multiple of 8, d and Hq * D at most 6400 (the rows that the "
+                             f"projections hold in shared memory): got D {D}, d {d}, Hq {Hq}")
         self.Hq, self.Hkv, self.D, self.inv_freq, self.interleaved = Hq, Hkv, D, inv_freq, interleaved
         f32 = dict(dtype=torch.float32, device=dev)
         self.x = torch.empty((T, d), **f32)

@@ -110,3 +110,11 @@ def test_a_released_stream_forgets_its_frames():
         c.advance()
         r.remember(torch.full((2, 2), i, dtype=torch.int32), idle=c.idle)
         assert kept(0) == list(range(max(7, i - 7), i + 1)) and kept(1) == list(range(max(0, i - 7), i + 1))
+
+
+def test_attention_runner_refuses_sizes_that_no_step_can_have():
+    from sparse_moe_decoder_b200 import AttentionRunner
+    AttentionRunner(2, 6400, 50, 2, 128, device="cpu")
+    for d, Hq, Hkv, D in ((6408, 16, 4, 128), (2048, 52, 4, 128), (2044, 16, 4, 128), (2048, 16, 4, 96), (0, 16, 4, 128)):
+        with pytest.raises(ValueError, match="6400"):
+            AttentionRunner(2, d, Hq, Hkv, D, device="cpu")
