@@ -173,8 +173,8 @@ class LogitRules:
     def __init__(self, T: int, N: int, window: int, repetition: Optional[torch.Tensor] = None,
                  presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
                  bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None, device="cuda"):
-        if window < 1:
-            raise ValueError("window must be at least 1")
+        if not 1 <= window <= 65535:
+            raise ValueError("window must be at least 1 and at most 65535")
         self.repetition, self.presence, self.frequency, self.bias, self.mask = repetition, presence, frequency, bias, mask
         self.history = torch.full((T, window, N), -1, dtype=torch.int32, device=device)
         self.hist_lens = torch.zeros(T, dtype=torch.int32, device=device)

@@ -118,3 +118,9 @@ def test_attention_runner_refuses_sizes_that_no_step_can_have():
     for d, Hq, Hkv, D in ((6408, 16, 4, 128), (2048, 52, 4, 128), (2044, 16, 4, 128), (2048, 16, 4, 96), (0, 16, 4, 128)):
         with pytest.raises(ValueError, match="6400"):
             AttentionRunner(2, d, Hq, Hkv, D, device="cpu")
+
+
+def test_a_window_has_no_more_frames_than_are_counted():
+    assert LogitRules(1, 1, 65535, device="cpu").history.shape == (1, 65535, 1)
+    with pytest.raises(ValueError, match="65535"):
+        LogitRules(1, 1, 65536, device="cpu")
