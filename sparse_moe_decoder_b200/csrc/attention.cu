@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, HT>::warps, 1)
     }
   }
   if (gave_up) {   // count it, and let the copies that may still come land before the memory is another's
-    if (lane == 0) atomicAdd(a.timeouts, 1u);
+    if (lane == 0) record_device_error(a.timeouts);   // null where the device has no counter
     for (int i = 0; i < L::slots; ++i) {
       mbar_wait(bar + slot, parity, &never, kWaitNs / 16);
       if (++slot == L::slots) {
