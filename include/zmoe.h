@@ -475,7 +475,7 @@ ZMOE_API zmoe_status zmoe_add_rmsnorm(const void* h, zmoe_dtype h_dtype, const v
  *   q_gamma, k_gamma: f32 [D] or NULL.  q_out: bf16 [T, Hq, D].
  *   k_cache, v_cache: [n_pages, Hkv, page_size, D] of kv_dtype (ZMOE_BF16, or ZMOE_E4M3: uint8 codes with
  *   k_scale, v_scale f32 [Hkv]); page_table: int32 [n_seqs, max_pages].
- *   A token with seq[t] < 0 is padding: nothing of it is stored.  A token whose sequence, position or page is out
+ *   A token with seq[t] < 0 is padding: nothing of it is stored, and its row of q_out stays as it was.  A token whose sequence, position or page is out
  *   of range counts a device error, and nothing of it is stored.  The (sequence, position) pairs of one call name
  *   different cache rows; a row named twice holds a mixture of the two tokens.
  *   D = 64 or 128 (else ZMOE_ERR_UNSUPPORTED), rotary_dim % 16 == 0, page_size % 16 == 0, 16-byte aligned pointers.
@@ -503,7 +503,9 @@ ZMOE_API size_t zmoe_paged_attention_workspace_size(int B, int Hq, int Hkv, int 
  *   is cut to that; the tokens of a page id outside [0, n_pages) count a device error and are left out.  When every
  *   token is left out (or scores -inf) the row is zeros and lse -inf.  What a page holds behind the sequence's end is
  *   read but never used, NaN included.
- *   fp32 accumulation; the results do not depend on the order in which CTAs finish.  Two launches on `stream`.  The
+ *   fp32 accumulation; the results do not depend on the order in which CTAs finish.  The weights exp(s - max) meet the
+ *   values in 16 bits for a bf16 output and in 24 for an f32 one; over an E4M3 cache in 22 bits, and a weight below
+ *   2^-39 of the largest does not count there.  Two launches on `stream`.  The
  *   workspace (16-byte aligned) belongs to one call at a time: calls that may overlap need one each.
  *   Hq % Hkv == 0, D = 64 or 128 (else ZMOE_ERR_UNSUPPORTED), page_size % 16 == 0, n_pages * Hkv * page_size < 2^31 - 1.
  */
@@ -524,7 +526,8 @@ ZMOE_API zmoe_status zmoe_paged_attention(const void* q, const void* k_cache, co
  *   ids[t, n] = the lowest v with the largest out among the ids that the mask allows and that are not NaN; -1 when
  *   there is none.
  *   logits, out: [T, N, V] of dtype (out may be logits); history: int32 [T, L, N] or NULL (frames of ids, oldest
- *   or newest first; a negative id is no id, an id >= V counts a device error and is left out); hist_lens: int32 [T]
+ *   or newest first; a negative id is no id, an id >= V counts a device error and is left out; it is read only where a
+ *   penalty is given); hist_lens: int32 [T]
  *   or NULL (= L), cut to [0, L]; repetition, presence, frequency: f32 [T] or NULL (that step is left out; any of them
  *   needs history); bias: f32 [N, V] or NULL; mask: bits of uint32 [T, N, ceil(V / 32)], id v at bit v % 32 of word
  *   v / 32, or NULL; ids: int32 [T, N] or NULL.  L <= 65535.  No workspace, one launch.

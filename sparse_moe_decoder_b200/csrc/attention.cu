@@ -11,8 +11,9 @@
 // a step, two steps), so 12 warps keep up to 192 KB an SM in flight, and no warp waits for another.
 //   scores  S = Q K^T:      m16n8k16, 16 rows of query heads (8 or 16 in use), 8 tokens, 16 columns;
 //   output  O^T = V^T P^T:  m16n8k16, 16 columns of V, 8 query heads, 16 tokens.
-// (A tcgen05 product has at least 64 rows, of which a group's heads would fill 4 or 8, and its accumulator lies in
-// tensor memory, from where the softmax would have to fetch it; the warp's product leaves S in registers.)
+// (A tcgen05 product has at least 64 rows, of which a group of 4 or 8 heads would fill as many, and its accumulator lies
+// in tensor memory, from where the softmax would have to fetch it; the warp's product leaves S in registers.  Groups of more
+// than 16 heads read the cache once for each 16 of them: 64 heads a group would fill such a product, which is not built.)
 // The contraction index of a tensor-core product may be permuted as long as both operands agree, so each lane's
 // share of a key row is 16-byte chunks, each lane's share of the output is 8 contiguous columns, and the swizzle
 // keeps both free of bank conflicts.  S leaves the first product in the layout that the second takes P^T in.  The
@@ -25,8 +26,8 @@
 // start early (programmatic dependent launch), joins what is left in a fixed order.
 //
 // Measured: 64 sequences of 1 to 4096 tokens (134k), 16 + 4 heads of 128, bf16: 55 us, 5.0 TB/s; 4 sequences, 286k
-// tokens, 32 + 4 heads of 128, E4M3: 61 us, 4.8 TB/s; one sequence of 431 tokens: 8.4 us; one of 20000 with 8 + 1 heads:
-// 14.8 us.  A longer cache adds at 6.1 (bf16) and 7 TB/s (E4M3); about 12 us are the two launches, the lengths' prefix,
+// tokens, 32 + 4 heads of 128, E4M3: 61 us, 4.8 TB/s; one sequence of 431 tokens: 8.5 us; one of 20000 with 8 + 1 heads:
+// 14.3 us.  A longer cache adds at 6.1 (bf16) and 7 TB/s (E4M3); about 12 us are the two launches, the lengths' prefix,
 // the first copies and the join.
 //
 // P is split into 16-bit terms, P = P_1 + P_2 (+ P_3), and the second product runs for each: one bf16 term alone would
@@ -250,7 +251,7 @@ __device__ __forceinline__ float gate_of(const AttnArgs& a, int b, int head) {
 
 // Do the CTAs of the first kernel join the parts of their warps?  It costs every CTA 2 to 3 us at its end, and saves the
 // second kernel a factor of 12 (or 8) where a group is cut into many parts: 27 parts a group took 8.3 us a call without
-// and 9.6 with, 7 parts 54.6 and 57.2, 111 parts 65.5 and 61.6, 1250 parts 71 and 15.
+// and 9.6 with, 7 parts 54.6 and 57.2, 111 parts 65.5 and 61.6, 1250 parts 71 and 14.3.
 __device__ __forceinline__ bool joined_early(const AttnArgs& a, const Pieces& pieces) {
   return pieces.count > 64LL * a.B * a.Hkv * a.gtiles;
 }

@@ -19,8 +19,9 @@
 // for the inputs and indices, then for the page's id.  One head in flight a group of lanes and four blocks an SM beat
 // two heads and three blocks (55 against 62 us below); eight tokens a block share the angles.
 //
-// Measured: 16384 tokens, 16 query and 4 key heads of 128, f32 into bf16: 55 us, 5.5 TB/s; 2997 tokens, 12 + 2 heads
-// of 64, bf16 into E4M3: 5.3 us, 2.2 TB/s; 64 tokens: 3.6 us a call.
+// Measured: 16384 tokens, 16 query and 4 key heads of 128, f32 into bf16: 54.8 us, 5.5 TB/s, into E4M3 52 us, 5.5 TB/s;
+// bf16 into either 45 us (4.4 and 4.1 TB/s); 2997 tokens, 12 + 2 heads of 64, bf16 into E4M3: 5.4 us, 2.1 TB/s; 64 tokens:
+// 3.6 us a call.
 #include "vectors.cuh"
 
 namespace zmoe {

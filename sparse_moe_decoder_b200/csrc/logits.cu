@@ -25,8 +25,9 @@
 // and a thread of its own takes it.
 //
 // Measured: 9 x 1025, 128 frames: 3.9 us a call; 576 rows of 1025 with 512 frames and masks: 7.0 us; 192 x 100003 bf16
-// with 2048 entries and masks: 45 us, of which the pass alone is 21.5 (a plain copy of these rows takes 19.7), biases and
-// masks 9, counting and settling 14 (102 us with the penalties within the pass).
+// with 2048 entries and masks: 45 us.  The pass alone takes 21.6 of them (its bytes at the copy rate 11.7, torch's copy of
+// these rows 18.6), with biases and masks 30.7, with the counting and settling and neither 37.1 (102 us with the penalties
+// within the pass).
 #include <type_traits>
 
 #include "sm100_ptx.cuh"
@@ -454,9 +455,10 @@ extern "C" zmoe_status zmoe_adjust_logits(const void* logits, zmoe_dtype dtype, 
   a.split = split;
   const int E = dtype == ZMOE_BF16 ? 8 : 4;
   const int vecs = ((V + 2 * E - 2) / E + split - 1) / split;
-  // Short rows take smaller CTAs, so that more of them run at once: always up to 512 vectors (576 rows of 1025 f32: 7.0 us
-  // against 9.4), up to 1024 where not all rows run at once anyway (1809 rows of 4039 f32: 18.3 against 26.5; one row of
-  // 6000: 5.9 against 5.4; 512 rows of 12000 bf16: 21.7 against 16.5).
+  // Short rows take smaller CTAs, so that more of them run at once: always up to 512 vectors (576 rows of 1025 f32 with
+  // biases and penalties: 6.9 us against 9.8), up to 1024 where not all rows run at once anyway (1809 rows of 4039 f32: 20.7
+  // against 28.6, but 270 of them 8.9 against 7.3; one row of 6000: 5.8 against 5.3; 512 rows of 12000 bf16: 20.4 against
+  // 16.7).
   const int threads = vecs <= 512 || (vecs <= 1024 && rows * split > static_cast<long long>(kBlocks) * num_sms()) ? 128 : 256;
   // As few chunks as fit shared memory beside the other CTAs of an SM (each takes the history anew) and a list of 16 bits.
   const int step = kAhead * threads;

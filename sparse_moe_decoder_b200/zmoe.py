@@ -643,6 +643,7 @@ def zmoe_kv_append(k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, k_cache:
                    k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
                    q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
     """Stores rotated keys and values in a paged cache; returns the rotated queries bf16 [T, Hq, D] (None without q).
+    The query rows of tokens that are not stored stay as they were: undefined where q_out is not given.
 
     q [T, Hq, D], k, v [T, Hkv, D]: f32 or bf16 views of a packed projection; pos int32 [T]; seq int32 [T] (None:
     token t is sequence t's; negative: padding); k_cache, v_cache [n_pages, Hkv, page_size, D] bf16, or uint8
